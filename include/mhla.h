@@ -462,6 +462,158 @@ mhla_status mhla_layer_forward(const void* x, const float* W, const mhla_grid* g
                                const mhla_layer_params* params, void* y, void* ws, size_t ws_bytes,
                                const hipEvent_t* stage_events, hipStream_t stream);
 
+/* ---------------------------------------------------------------- gated linear attention
+ *
+ * The causal linear attention whose memory is one d x d state for each
+ * key-value head, with a gate for every token instead of a coefficient for
+ * every pair of chunks:
+ *
+ *   S_t = exp(g_t) S_{t-1} + k_t v_t^T,    o_t = scale * S_t^T q_t
+ *
+ * so that o_t = scale * sum_{s <= t} exp(g_{s+1} + .. + g_t) (q_t . k_s) v_s
+ * plus what the initial state gives.  There is no feature map and no
+ * normaliser: q and k enter as they are.  A sequence is computed in chunks of
+ * 64 tokens on the matrix cores and, where there are few heads, in segments
+ * that are joined; a token at a time (mhla_gated_step) gives the same states.
+ *
+ * Tensors (device pointers):
+ *   q, dq, out, dout  [B, T, H, d]     k, v, dk, dv  [B, T, Hk, d]
+ *   g, dg             [B, T, Hk] fp32  (log gates: -infinity forgets the state,
+ *                                       so it starts a sequence of its own)
+ *   states            [B, Hk, d, d] fp32, element [c][e] from key value c and
+ *                     value value e
+ *   lens              [B] int32 or NULL: sequence b has min(max(lens[b], 0), T)
+ *                     tokens.  What the inputs hold behind them is not used
+ *                     (whatever it is); out, dq, dk, dv and dg are zero there,
+ *                     and the final state is the one after the last token.
+ * Heads h of q share the state, k and v of head h / (H / Hk); H is a multiple
+ * of Hk.  q, k and v may be slices of a wider row (strides below); all other
+ * tensors are contiguous.  A value that is not finite reaches the outputs of
+ * its own chunk (64 tokens, counted from the sequence's start), earlier tokens
+ * among them, and of all later tokens, past a gate of 0 too; never those of
+ * another sequence.
+ *
+ * Precision: states, gate sums and dg are fp32 sums of products as precise as
+ * in fp32; bf16 tensors are rounded once, at the end.  No atomics: results
+ * are the same on every call. */
+
+typedef struct mhla_seq {
+    int32_t batch;       /* B >= 0 */
+    int32_t tokens;      /* T in [0, 2^30] */
+    int32_t heads;       /* H in [0, 65536] */
+    int32_t kv_heads;    /* Hk, divides H */
+    int32_t head_dim;    /* d: 32, 64 or 128 */
+    int32_t dtype;       /* mhla_dtype of q, k, v, out and their gradients */
+    int64_t q_stride;    /* values between a token's q and the next token's; 0: H * d.  At least */
+    int64_t k_stride;    /*   the heads' own values, and a multiple of 16 bytes.  A batch item is */
+    int64_t v_stride;    /*   T tokens: item b starts at token b * T. */
+    float scale;         /* finite */
+} mhla_seq;
+
+/* Validates a sequence problem alone: MHLA_OK, MHLA_ERR_INVALID_ARG (negative
+ * counts, H % Hk != 0, a stride below the heads' values, scale not finite),
+ * MHLA_ERR_MISALIGNED (a stride that is no multiple of 16 bytes) or
+ * MHLA_ERR_UNSUPPORTED (head_dim, dtype, or a size past the limits above or
+ * past 2^31 - 1 workgroups). */
+mhla_status mhla_check_seq(const mhla_seq* seq);
+
+/* Bytes of device workspace (0 for an invalid problem, an empty batch, or a
+ * problem that needs none).  From the start, at 256-byte boundaries, for the
+ * segments a sequence is split into: states before each segment and after the
+ * last, segment decays, and backwards the states' gradients behind each
+ * segment and the per-token sums that dg is made of. */
+size_t mhla_gated_workspace_bytes(const mhla_seq* seq);
+size_t mhla_gated_backward_workspace_bytes(const mhla_seq* seq);
+
+/* The forward pass.  state: the initial state or NULL (zero).  state_out:
+ * receives the final state, or NULL; may be `state` itself.  ws: a workspace
+ * of ws_bytes >= mhla_gated_workspace_bytes (16-byte aligned; any pointer if
+ * that is 0), or NULL with ws_bytes 0 to allocate it on the stream
+ * (hipMallocAsync / hipFreeAsync).  Asynchronous on `stream`; T = 0 only
+ * copies the state.  g and lens need 4-byte alignment, the other pointers 16.
+ * Outputs may not overlap inputs, each other or the workspace, but for the
+ * state. */
+mhla_status mhla_gated_forward(const void* q, const void* k, const void* v, const float* g, const int32_t* lens,
+                               const float* state, const mhla_seq* seq, void* out, float* state_out, void* ws,
+                               size_t ws_bytes, hipStream_t stream);
+
+/* Gradients of a scalar L given dout = dL/dout and, if not NULL,
+ * dstate_out = dL/d(state_out).  With D_t = dL/dS_t:
+ *
+ *   D_t  = scale * q_t dout_t^T (summed over the heads that share the state) + exp(g_{t+1}) D_{t+1}
+ *   dq_t = scale * S_t dout_t,  dk_t = D_t v_t,  dv_t = D_t^T k_t
+ *   dg_t = exp(g_t) <S_{t-1}, D_t>,  dstate = exp(g_1) D_1
+ *
+ * dq, dk, dv in the problem's dtype, contiguous; dg fp32 (zero where exp(g) is
+ * zero in fp32); dstate: the initial state's gradient or NULL; it may be
+ * dstate_out itself.  The states are recomputed.  Other arguments and rules as
+ * for mhla_gated_forward. */
+mhla_status mhla_gated_backward(const void* q, const void* k, const void* v, const float* g, const int32_t* lens,
+                                const float* state, const void* dout, const float* dstate_out, const mhla_seq* seq,
+                                void* dq, void* dk, void* dv, float* dg, float* dstate, void* ws, size_t ws_bytes,
+                                hipStream_t stream);
+
+/* One new token for each of B rows (seq->tokens must be 1; strides are those
+ * between rows): q, out [B, H, d], k, v [B, Hk, d], g [B, Hk].  state: a pool
+ * [num_slots, Hk, d, d], updated in place.  slots: [B] int32, the pool's entry
+ * of each row, or NULL for entry b (then num_slots >= B).  A row whose slot is
+ * outside [0, num_slots) changes no state and gets zeros.  Rows with the same
+ * slot are consecutive tokens of that sequence, in the order of the rows.
+ * Needs no workspace. */
+mhla_status mhla_gated_step(const void* q, const void* k, const void* v, const float* g, const int32_t* slots,
+                            const mhla_seq* seq, float* state, int32_t num_slots, void* out, hipStream_t stream);
+
+/* ---------------------------------------------------------------- query/key norm and rotation
+ *
+ * What makes the q and k of an attention layer out of its projections, in one
+ * pass: for every token and head
+ *
+ *   u = x / sqrt(mean(x^2) + eps),  n = w u  (w: fp32 [d], NULL for ones)
+ *
+ * and the pairs of n turned by the token's positions: pair (a, b) becomes
+ * (a cos th - b sin th, b cos th + a sin th), th = position * freq[pair].
+ * The P = section[0] + section[1] + section[2] pairs go to the axes in order:
+ * the first section[0] turn with the token's first position, and so on (image
+ * and video grids; a sequence has one axis).  Values from 2 P on are only
+ * normalised.  Positions are any int32; angles are formed in 64 bits. */
+
+enum {
+    MHLA_ROPE_HALVES = 0,       /* pair i: values i and P + i */
+    MHLA_ROPE_INTERLEAVED = 1   /* pair i: values 2 i and 2 i + 1 */
+};
+
+typedef struct mhla_rope {
+    int32_t style;         /* MHLA_ROPE_* */
+    int32_t axes;          /* positions of a token: 1, 2 or 3 */
+    int32_t section[3];    /* pairs of each axis, >= 0, 0 past `axes`; their sum P is a positive
+                              multiple of 8, at most d / 2 */
+    float eps;             /* finite, > 0 */
+} mhla_rope;
+
+/* q [B, T, H, d], k [B, T, Hk, d] in seq's dtype and strides (v_stride and
+ * scale are not used; kv_heads need not divide heads); positions
+ * [B, T, axes] int32; freq [P] fp32; q_out, k_out contiguous.  q_out may be q
+ * itself, and k_out k, where these are contiguous.  positions and freq need
+ * 4-byte alignment, the other pointers 16.  Needs no workspace. */
+mhla_status mhla_qk_norm_rope(const void* q, const void* k, const float* w_q, const float* w_k,
+                              const int32_t* positions, const float* freq, const mhla_rope* rope,
+                              const mhla_seq* seq, void* q_out, void* k_out, hipStream_t stream);
+
+/* Bytes of device workspace of the backward pass (partial sums of dw_q, dw_k). */
+size_t mhla_qk_norm_rope_backward_workspace_bytes(const mhla_seq* seq);
+
+/* Gradients: with dn the gradient of the rotated n turned back,
+ * dw = sum over tokens and heads of dn u and dx = (w dn - u mean(w dn u)) / sqrt(mean(x^2) + eps).
+ * dq_out, dk_out: gradients of q_out, k_out (contiguous, read); dq, dk
+ * contiguous (dq may be dq_out itself, dk dk_out); dw_q, dw_k: fp32 [d] or
+ * NULL, overwritten (zero for an empty problem).  q and k are the forward's
+ * inputs.  ws as for mhla_gated_forward. */
+mhla_status mhla_qk_norm_rope_backward(const void* q, const void* k, const float* w_q, const float* w_k,
+                                       const int32_t* positions, const float* freq, const mhla_rope* rope,
+                                       const void* dq_out, const void* dk_out, const mhla_seq* seq, void* dq,
+                                       void* dk, float* dw_q, float* dw_k, void* ws, size_t ws_bytes,
+                                       hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

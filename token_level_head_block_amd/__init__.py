@@ -42,6 +42,9 @@ MHLA_VARIANT_APPLY_REGS = 1 << 12
 MHLA_PHI_ELU1 = 0
 MHLA_PHI_RELU_EPS = 1
 
+MHLA_ROPE_HALVES = 0
+MHLA_ROPE_INTERLEAVED = 1
+
 
 class mhla_grid(ctypes.Structure):
     _fields_ = [("batch", ctypes.c_int32), ("heads", ctypes.c_int32),
@@ -60,6 +63,18 @@ class mhla_layer_params(ctypes.Structure):
                 ("lepe_w", ctypes.c_void_p), ("lepe_b", ctypes.c_void_p), ("w_out", ctypes.c_void_p),
                 ("b_out", ctypes.c_void_p), ("phi", ctypes.c_int32), ("phi_eps", ctypes.c_float),
                 ("ln_eps", ctypes.c_float), ("rms_eps", ctypes.c_float)]
+
+
+class mhla_seq(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("tokens", ctypes.c_int32), ("heads", ctypes.c_int32),
+                ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64),
+                ("scale", ctypes.c_float)]
+
+
+class mhla_rope(ctypes.Structure):
+    _fields_ = [("style", ctypes.c_int32), ("axes", ctypes.c_int32), ("section", ctypes.c_int32 * 3),
+                ("eps", ctypes.c_float)]
 
 
 class MhlaError(RuntimeError):
@@ -122,6 +137,23 @@ def lib() -> ctypes.CDLL:
         L.mhla_layer_forward.argtypes = [vp, vp, G, Bk, ctypes.POINTER(mhla_layer_params), vp, vp,
                                          ctypes.c_size_t, vp, vp]
         L.mhla_layer_forward.restype = ctypes.c_int
+        Sq, Rp = ctypes.POINTER(mhla_seq), ctypes.POINTER(mhla_rope)
+        L.mhla_check_seq.argtypes = [Sq]
+        L.mhla_check_seq.restype = ctypes.c_int
+        for f in (L.mhla_gated_workspace_bytes, L.mhla_gated_backward_workspace_bytes,
+                  L.mhla_qk_norm_rope_backward_workspace_bytes):
+            f.argtypes = [Sq]
+            f.restype = ctypes.c_size_t
+        L.mhla_gated_forward.argtypes = [vp] * 6 + [Sq, vp, vp, vp, ctypes.c_size_t, vp]
+        L.mhla_gated_forward.restype = ctypes.c_int
+        L.mhla_gated_backward.argtypes = [vp] * 8 + [Sq, vp, vp, vp, vp, vp, vp, ctypes.c_size_t, vp]
+        L.mhla_gated_backward.restype = ctypes.c_int
+        L.mhla_gated_step.argtypes = [vp] * 5 + [Sq, vp, ctypes.c_int32, vp, vp]
+        L.mhla_gated_step.restype = ctypes.c_int
+        L.mhla_qk_norm_rope.argtypes = [vp] * 6 + [Rp, Sq, vp, vp, vp]
+        L.mhla_qk_norm_rope.restype = ctypes.c_int
+        L.mhla_qk_norm_rope_backward.argtypes = [vp] * 6 + [Rp, vp, vp, Sq, vp, vp, vp, vp, vp, ctypes.c_size_t, vp]
+        L.mhla_qk_norm_rope_backward.restype = ctypes.c_int
         _lib = L
     return _lib
 
@@ -399,3 +431,283 @@ def mhla_layer_forward(x, W, grid: mhla_grid, block: mhla_block, params: dict, y
     P.phi, P.phi_eps, P.ln_eps, P.rms_eps = int(phi), float(phi_eps), float(ln_eps), float(rms_eps)
     return lib().mhla_layer_forward(_ptr(x), _ptr(W), ctypes.byref(grid), ctypes.byref(block), ctypes.byref(P),
                                     _ptr(y), _ptr(ws), int(ws_bytes), _events(stage_events, 5), _stream(stream))
+
+
+# ---------------------------------------------------------------- gated linear attention, q/k norm and rotation
+
+def make_seq(batch: int, tokens: int, heads: int, kv_heads: int, head_dim: int, dtype: int, scale: float = 1.0,
+             q_stride: int = 0, k_stride: int = 0, v_stride: int = 0) -> mhla_seq:
+    return mhla_seq(batch, tokens, heads, kv_heads, head_dim, dtype, q_stride, k_stride, v_stride, scale)
+
+
+def make_rope(sections, style: int = MHLA_ROPE_HALVES, eps: float = 1e-6) -> mhla_rope:
+    """sections: the pairs that turn with each axis's position, one entry an axis (1 to 3)."""
+    n = len(sections)
+    r = mhla_rope(int(style), n, (0, 0, 0), float(eps))
+    for a in range(min(n, 3)):
+        r.section[a] = int(sections[a])
+    return r
+
+
+def mhla_check_seq(seq: mhla_seq) -> int:
+    return lib().mhla_check_seq(ctypes.byref(seq))
+
+
+def mhla_gated_workspace_bytes(seq: mhla_seq) -> int:
+    return int(lib().mhla_gated_workspace_bytes(ctypes.byref(seq)))
+
+
+def mhla_gated_backward_workspace_bytes(seq: mhla_seq) -> int:
+    return int(lib().mhla_gated_backward_workspace_bytes(ctypes.byref(seq)))
+
+
+def mhla_qk_norm_rope_backward_workspace_bytes(seq: mhla_seq) -> int:
+    return int(lib().mhla_qk_norm_rope_backward_workspace_bytes(ctypes.byref(seq)))
+
+
+def _need(name, t, shape, dtype, device):
+    """A contiguous GPU tensor of this shape and type on `device`."""
+    if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, "
+                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+
+
+def _stride_of(name, t, shape, dtype, device):
+    """Values between a token of t and the next one, for a tensor [B, T, heads, d] whose tokens' values
+    are contiguous and evenly spaced over the whole batch (a slice of a wider row, say)."""
+    if t.shape != shape or t.dtype != dtype or t.device != device:
+        raise ValueError(f"{name} must be a {dtype} tensor of shape {tuple(shape)} on {device}, "
+                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+    B, T, h, d = shape
+    if t.is_contiguous():
+        return h * d
+    sb, st, sh, sd = t.stride()
+    step = st if T > 1 else sb if B > 1 else h * d
+    if sd != 1 or (h > 1 and sh != d) or (T > 1 and B > 1 and sb != T * st) or step < h * d:
+        raise ValueError(f"{name}: the values of a token must be contiguous and tokens evenly spaced, "
+                         f"got strides {t.stride()} for shape {tuple(shape)}")
+    return step
+
+
+def _check_seq_tensors(q, k, v, seq: mhla_seq):
+    """The type and device of a sequence problem's tensors, after checking q, k and v (or None) against seq.
+    The C ABI cannot see tensor sizes."""
+    import torch
+    dt = torch.bfloat16 if seq.dtype == MHLA_BF16 else torch.float32
+    dev = q.device
+    if dev.type != "cuda":
+        raise ValueError("q must be on a GPU")
+    B, T, H, Hk, d = seq.batch, seq.tokens, seq.heads, seq.kv_heads, seq.head_dim
+    for name, t, h, stride in (("q", q, H, seq.q_stride), ("k", k, Hk, seq.k_stride), ("v", v, Hk, seq.v_stride)):
+        if t is None:
+            continue
+        s = _stride_of(name, t, (B, T, h, d), dt, dev)
+        if B * T > 1 and s != (stride or h * d):
+            raise ValueError(f"{name}: a token stride of {s} where seq has {stride or h * d}")
+    return dt, dev
+
+
+def _check_workspace(ws, ws_bytes, device):
+    if hasattr(ws, "numel"):
+        if not ws.is_contiguous() or ws.device != device or ws.numel() * ws.element_size() < ws_bytes:
+            raise ValueError(f"ws must be a contiguous tensor of at least ws_bytes = {ws_bytes} bytes on {device}")
+
+
+def _call(fn, device, stream, *args) -> int:
+    """fn(*args, stream) with `device` current; stream: None for its current one."""
+    import torch
+    if stream is None:
+        s = torch.cuda.current_stream(device).cuda_stream
+    else:
+        s = stream if isinstance(stream, int) else stream.cuda_stream
+    if device.index == torch.cuda.current_device():
+        return fn(*args, s)
+    with torch.cuda.device(device):
+        return fn(*args, s)
+
+
+def mhla_gated_forward(q, k, v, g, seq: mhla_seq, out, lens=None, state=None, state_out=None, ws=None,
+                       ws_bytes: int = 0, stream=None) -> int:
+    """The C entry point with torch tensors: q, out [B, T, H, d], k, v [B, T, Hk, d], g fp32 [B, T, Hk],
+    lens int32 [B] or None, state and state_out fp32 [B, Hk, d, d] or None."""
+    import torch
+    dt, dev = _check_seq_tensors(q, k, v, seq)
+    B, T, H, Hk, d = seq.batch, seq.tokens, seq.heads, seq.kv_heads, seq.head_dim
+    _need("g", g, (B, T, Hk), torch.float32, dev)
+    _need("out", out, (B, T, H, d), dt, dev)
+    if lens is not None:
+        _need("lens", lens, (B,), torch.int32, dev)
+    for name, t in (("state", state), ("state_out", state_out)):
+        if t is not None:
+            _need(name, t, (B, Hk, d, d), torch.float32, dev)
+    _check_workspace(ws, ws_bytes, dev)
+    return _call(lib().mhla_gated_forward, dev, stream, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(lens), _ptr(state),
+                 ctypes.byref(seq), _ptr(out), _ptr(state_out), _ptr(ws), ws_bytes)
+
+
+def mhla_gated_backward(q, k, v, g, dout, seq: mhla_seq, dq, dk, dv, dg, lens=None, state=None, dstate_out=None,
+                        dstate=None, ws=None, ws_bytes: int = 0, stream=None) -> int:
+    """Gradients through mhla_gated_forward: dq, dk, dv like q, k, v (contiguous), dg like g; dstate_out is the
+    final state's gradient (or None), dstate receives the initial state's (or None)."""
+    import torch
+    dt, dev = _check_seq_tensors(q, k, v, seq)
+    B, T, H, Hk, d = seq.batch, seq.tokens, seq.heads, seq.kv_heads, seq.head_dim
+    for name, t in (("dout", dout), ("dq", dq)):
+        _need(name, t, (B, T, H, d), dt, dev)
+    for name, t in (("dk", dk), ("dv", dv)):
+        _need(name, t, (B, T, Hk, d), dt, dev)
+    for name, t in (("g", g), ("dg", dg)):
+        _need(name, t, (B, T, Hk), torch.float32, dev)
+    if lens is not None:
+        _need("lens", lens, (B,), torch.int32, dev)
+    for name, t in (("state", state), ("dstate_out", dstate_out), ("dstate", dstate)):
+        if t is not None:
+            _need(name, t, (B, Hk, d, d), torch.float32, dev)
+    _check_workspace(ws, ws_bytes, dev)
+    return _call(lib().mhla_gated_backward, dev, stream, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(lens), _ptr(state),
+                 _ptr(dout), _ptr(dstate_out), ctypes.byref(seq), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dg),
+                 _ptr(dstate), _ptr(ws), ws_bytes)
+
+
+def mhla_gated_step(q, k, v, g, seq: mhla_seq, state, out, slots=None, stream=None) -> int:
+    """One token a row: q, out [B, H, d], k, v [B, Hk, d], g fp32 [B, Hk], state fp32 [num_slots, Hk, d, d]
+    (updated in place), slots int32 [B] or None (row b has entry b)."""
+    import torch
+    dt, dev = _check_seq_tensors(q.unsqueeze(1), k.unsqueeze(1), v.unsqueeze(1), seq)
+    B, H, Hk, d = seq.batch, seq.heads, seq.kv_heads, seq.head_dim
+    _need("g", g, (B, Hk), torch.float32, dev)
+    _need("out", out, (B, H, d), dt, dev)
+    if slots is not None:
+        _need("slots", slots, (B,), torch.int32, dev)
+    n = state.shape[0]
+    _need("state", state, (n, Hk, d, d), torch.float32, dev)
+    return _call(lib().mhla_gated_step, dev, stream, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(slots),
+                 ctypes.byref(seq), _ptr(state), n, _ptr(out))
+
+
+def _check_rope_tensors(q, k, w_q, w_k, positions, freq, rope: mhla_rope, seq: mhla_seq):
+    import torch
+    dt, dev = _check_seq_tensors(q, k, None, seq)
+    d = seq.head_dim
+    _need("positions", positions, (seq.batch, seq.tokens, rope.axes), torch.int32, dev)
+    _need("freq", freq, (rope.section[0] + rope.section[1] + rope.section[2],), torch.float32, dev)
+    for name, t in (("w_q", w_q), ("w_k", w_k)):
+        if t is not None:
+            _need(name, t, (d,), torch.float32, dev)
+    return dt, dev
+
+
+def mhla_qk_norm_rope(q, k, w_q, w_k, positions, freq, rope: mhla_rope, seq: mhla_seq, q_out, k_out,
+                      stream=None) -> int:
+    """q, q_out [B, T, H, d], k, k_out [B, T, Hk, d], w_q, w_k fp32 [d] or None, positions int32 [B, T, axes],
+    freq fp32 [pairs]."""
+    dt, dev = _check_rope_tensors(q, k, w_q, w_k, positions, freq, rope, seq)
+    _need("q_out", q_out, q.shape, dt, dev)
+    _need("k_out", k_out, k.shape, dt, dev)
+    return _call(lib().mhla_qk_norm_rope, dev, stream, _ptr(q), _ptr(k), _ptr(w_q), _ptr(w_k), _ptr(positions),
+                 _ptr(freq), ctypes.byref(rope), ctypes.byref(seq), _ptr(q_out), _ptr(k_out))
+
+
+def mhla_qk_norm_rope_backward(q, k, w_q, w_k, positions, freq, rope: mhla_rope, dq_out, dk_out, seq: mhla_seq, dq,
+                               dk, dw_q=None, dw_k=None, ws=None, ws_bytes: int = 0, stream=None) -> int:
+    """Gradients through mhla_qk_norm_rope; dw_q, dw_k fp32 [d] or None."""
+    import torch
+    dt, dev = _check_rope_tensors(q, k, w_q, w_k, positions, freq, rope, seq)
+    for name, t, like in (("dq_out", dq_out, q), ("dq", dq, q), ("dk_out", dk_out, k), ("dk", dk, k)):
+        _need(name, t, like.shape, dt, dev)
+    for name, t in (("dw_q", dw_q), ("dw_k", dw_k)):
+        if t is not None:
+            _need(name, t, (seq.head_dim,), torch.float32, dev)
+    _check_workspace(ws, ws_bytes, dev)
+    return _call(lib().mhla_qk_norm_rope_backward, dev, stream, _ptr(q), _ptr(k), _ptr(w_q), _ptr(w_k),
+                 _ptr(positions), _ptr(freq), ctypes.byref(rope), _ptr(dq_out), _ptr(dk_out), ctypes.byref(seq),
+                 _ptr(dq), _ptr(dk), _ptr(dw_q), _ptr(dw_k), _ptr(ws), ws_bytes)
+
+
+def _seq_of(q, k, v, scale=None) -> mhla_seq:
+    """The sequence problem of tensors q [B, T, H, d], k and v [B, T, Hk, d] (v or None)."""
+    import torch
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError("q, k and v must be [batch, tokens, heads, head_dim]")
+    dt = {torch.bfloat16: MHLA_BF16, torch.float32: MHLA_F32}.get(q.dtype)
+    if dt is None:
+        raise ValueError(f"q must be bfloat16 or float32, got {q.dtype}")
+    B, T, H, d = q.shape
+    Hk = k.shape[2]
+    strides = [_stride_of(n, t, (B, T, h, d), q.dtype, q.device) if t is not None else 0
+               for n, t, h in (("q", q, H), ("k", k, Hk), ("v", v, Hk))]
+    return make_seq(B, T, H, Hk, d, dt, d ** -0.5 if scale is None else scale, *strides)
+
+
+def _workspace(n, like):
+    import torch
+    return torch.empty(n, dtype=torch.uint8, device=like.device) if n else None
+
+
+def _raise(st, what):
+    if st != MHLA_OK:
+        raise MhlaError(st, what)
+
+
+def gated_forward(q, k, v, g, scale=None, state=None, lens=None, want_state: bool = False):
+    """Gated linear attention over a sequence: S_t = exp(g_t) S_{t-1} + k_t v_t^T, out_t = scale S_t^T q_t
+    (scale: head_dim ** -0.5 by default).  Returns out, and with want_state (out, the final state).  Runs on the
+    current stream of the tensors' device; tensors as for mhla_gated_forward."""
+    import torch
+    seq = _seq_of(q, k, v, scale)
+    out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    new = None
+    if want_state:
+        new = torch.empty(seq.batch, seq.kv_heads, seq.head_dim, seq.head_dim, dtype=torch.float32, device=q.device)
+    n = mhla_gated_workspace_bytes(seq)
+    _raise(mhla_gated_forward(q, k, v, g, seq, out, lens, state, new, _workspace(n, q), n), "mhla_gated_forward")
+    return (out, new) if want_state else out
+
+
+def gated_backward(q, k, v, g, dout, scale=None, state=None, dstate=None, lens=None):
+    """(dq, dk, dv, dg, gradient of the initial state) of gated_forward, given dout and, if not None, dstate, the
+    final state's gradient.  The last one is None where state is."""
+    import torch
+    seq = _seq_of(q, k, v, scale)
+    dq, dk, dv = (torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q, k, v))
+    dg = torch.empty_like(g)
+    dstart = None if state is None else torch.empty_like(state)
+    n = mhla_gated_backward_workspace_bytes(seq)
+    _raise(mhla_gated_backward(q, k, v, g, dout, seq, dq, dk, dv, dg, lens, state, dstate, dstart, _workspace(n, q),
+                               n), "mhla_gated_backward")
+    return dq, dk, dv, dg, dstart
+
+
+def gated_step(q, k, v, g, state, scale=None, slots=None):
+    """One token for each row: q [B, H, d], k, v [B, Hk, d], g [B, Hk]; state [num_slots, Hk, d, d] is updated in
+    place.  Returns out [B, H, d].  slots as for mhla_gated_step."""
+    import torch
+    seq = _seq_of(q.unsqueeze(1), k.unsqueeze(1), v.unsqueeze(1), scale)
+    out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    _raise(mhla_gated_step(q, k, v, g, seq, state, out, slots), "mhla_gated_step")
+    return out
+
+
+def qk_norm_rope(q, k, w_q, w_k, positions, freq, sections=None, style: int = MHLA_ROPE_HALVES, eps: float = 1e-6):
+    """RMSNorm of every head of q and k with weights w_q, w_k (or None), and the rotation by the tokens'
+    positions.  sections: pairs of each axis (one axis for all of freq by default).  Returns (q, k)."""
+    import torch
+    seq = _seq_of(q, k, None, 1.0)
+    rope = make_rope(sections if sections is not None else (freq.numel(),), style, eps)
+    qo, ko = (torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q, k))
+    _raise(mhla_qk_norm_rope(q, k, w_q, w_k, positions, freq, rope, seq, qo, ko), "mhla_qk_norm_rope")
+    return qo, ko
+
+
+def qk_norm_rope_backward(q, k, w_q, w_k, positions, freq, sections, dq_out, dk_out, style: int = MHLA_ROPE_HALVES,
+                          eps: float = 1e-6):
+    """(dq, dk, dw_q, dw_k) of qk_norm_rope; a weight's gradient is None where the weight is."""
+    import torch
+    seq = _seq_of(q, k, None, 1.0)
+    rope = make_rope(sections if sections is not None else (freq.numel(),), style, eps)
+    dq, dk = (torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q, k))
+    dw = [None if w is None else torch.empty_like(w) for w in (w_q, w_k)]
+    n = mhla_qk_norm_rope_backward_workspace_bytes(seq)
+    _raise(mhla_qk_norm_rope_backward(q, k, w_q, w_k, positions, freq, rope, dq_out, dk_out, seq, dq, dk, *dw,
+                                      _workspace(n, q), n), "mhla_qk_norm_rope_backward")
+    return dq, dk, *dw

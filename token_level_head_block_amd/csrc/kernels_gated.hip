@@ -1,0 +1,1055 @@
+// kernels_gated.hip -- gated linear attention: a state S [d, d] for every
+// key-value head, S_t = exp(g_t) S_{t-1} + k_t v_t^T, o_t = scale S_t^T q_t.
+//
+// Chunk form.  With G the running sum of the gates inside a chunk of 64 tokens
+// and S the state before it,
+//   o_t  = scale (exp(G_t) S^T q_t + sum_{s <= t} exp(G_t - G_s) (q_t . k_s) v_s)
+//   S'   = exp(G_end) S + sum_s exp(G_end - G_s) k_s v_s^T.
+// All three gradients have the same form with the roles exchanged.  A walk has
+// a query role X, a key role Y and a value role Z:
+//   out: X = q, Y = k, Z = v, forwards        dq: X = do, Y = v, Z = k, forwards
+//   dv:  X = k, Y = q, Z = do, backwards      dk: X = v, Y = do, Z = q, backwards
+// (backwards: token s sees the tokens t >= s with exp(G_t - G_s), the state
+// holds the tokens behind the chunk and is taken with exp(G_end - G_s)).
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "common.h"
+#include "gated.h"
+
+namespace mhla {
+namespace {
+
+constexpr int GC = GATED_CHUNK;
+constexpr int THREADS = 256;
+constexpr float LOG2E = 1.44269504088896341f;
+constexpr float LOG2E_LOW = 1.92596299e-8f;    // log2(e) - LOG2E
+
+// ---------------------------------------------------------------- operands
+// A 16-row operand over 32 contraction values: lane (g = lane / 16, i = lane % 16)
+// holds row i's values in one of two orders, the same for both operands of a product:
+// "row" order, 8g + j (j < 8), or "token" order, 16 (j / 4) + 4g + j % 4, in which a
+// pair of accumulator tiles (rows 4g + 0..3 of column i) is an operand as it stands.
+// bf16: one 16x16x32 product; fp32: eight 16x16x4 products.
+template <typename E>
+struct Frag;
+template <>
+struct Frag<uint16_t> {
+    u32x4 v;
+};
+template <>
+struct Frag<float> {
+    f32x4 a, b;
+};
+
+__device__ __forceinline__ f32x4 mma(const Frag<uint16_t>& a, const Frag<uint16_t>& b, const f32x4& c) {
+    return mfma_bf16(a.v, b.v, c);
+}
+__device__ __forceinline__ f32x4 mma(const Frag<float>& a, const Frag<float>& b, f32x4 c) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) c = mfma_f32(a.a[j], b.a[j], c);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) c = mfma_f32(a.b[j], b.b[j], c);
+    return c;
+}
+
+// Eight fp32 values as the sum of N operands.  bf16: each rounded to nearest, the
+// remainder to the next (the subtractions are exact): one keeps 8 significant bits,
+// two 17, three all 24.
+template <int N>
+__device__ __forceinline__ void split(const float (&x)[8], Frag<uint16_t> (&f)[N]) {
+    float r[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) r[j] = x[j];
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t w = pack_bf16(r[2 * j], r[2 * j + 1]);
+            f[n].v[j] = w;
+            if (n + 1 < N) {
+                r[2 * j] -= bf_lo(w);
+                r[2 * j + 1] -= bf_hi(w);
+            }
+        }
+    }
+}
+template <int N>
+__device__ __forceinline__ void split(const float (&x)[8], Frag<float> (&f)[N]) {
+    static_assert(N == 1, "fp32 operands need no split");
+    f[0].a = f32x4{x[0], x[1], x[2], x[3]};
+    f[0].b = f32x4{x[4], x[5], x[6], x[7]};
+}
+
+__device__ __forceinline__ void widen(const Frag<uint16_t>& f, float (&x)[8]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        x[2 * j] = bf_lo(f.v[j]);
+        x[2 * j + 1] = bf_hi(f.v[j]);
+    }
+}
+__device__ __forceinline__ void widen(const Frag<float>& f, float (&x)[8]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        x[j] = f.a[j];
+        x[4 + j] = f.b[j];
+    }
+}
+
+// ---------------------------------------------------------------- tiles in LDS
+// Rows of W values, in 16-byte pieces whose place in the row is XORed with a number of
+// the row, so that the lanes of a read that hold 16 rows of one piece (row order) or 4
+// or 8 rows of two neighbouring pieces (token order) fall on different banks.
+template <typename E, int W>
+struct Tile {
+    static constexpr int ROWB = W * (int)sizeof(E);
+    static constexpr int NP = ROWB / 16;
+    static constexpr int RP = ROWB >= 256 ? 1 : 256 / ROWB;   // rows in a pass over all banks
+
+    __device__ static __forceinline__ int at(int row, int piece) {
+        int f;
+        if constexpr (sizeof(E) == 2) {
+            const int m = (row / RP) & (NP - 1);
+            f = ((m & (NP / 2 - 1)) << 1) | (m / (NP / 2));
+        } else {
+            f = (row / RP) & ((NP < 16 ? NP : 16) - 1);
+        }
+        return row * ROWB + ((piece ^ f) << 4);
+    }
+    // 16 rows from row0, contraction over columns 32 kk .. 32 kk + 31, row order
+    __device__ static __forceinline__ Frag<E> rows(const char* t, int row0, int kk, int lane) {
+        const int row = row0 + (lane & 15), g = lane >> 4;
+        Frag<E> f;
+        if constexpr (sizeof(E) == 2) {
+            f.v = *reinterpret_cast<const u32x4*>(t + at(row, 4 * kk + g));
+        } else {
+            f.a = *reinterpret_cast<const f32x4*>(t + at(row, 8 * kk + 2 * g));
+            f.b = *reinterpret_cast<const f32x4*>(t + at(row, 8 * kk + 2 * g + 1));
+        }
+        return f;
+    }
+    // columns 16 n .. 16 n + 15, contraction over rows 32 kk .. 32 kk + 31, token order
+    __device__ static __forceinline__ Frag<E> cols(const char* t, int kk, int n, int lane) {
+        const int i = lane & 15, g = lane >> 4;
+        Frag<E> f;
+        if constexpr (sizeof(E) == 2) {
+            // transposing reads: in a group of 16 lanes, 4 lanes address the 32 bytes of one row,
+            // lane i gets column i of the group's 4 rows
+            typedef short s16x4 __attribute__((ext_vector_type(4)));
+            typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+            const int row = 32 * kk + 4 * g + (i >> 2), piece = 2 * n + ((i & 3) >> 1), half = (i & 1) * 8;
+            const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(t + at(row, piece) + half));
+            const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(t + at(row + 16, piece) + half));
+            const u32x2 ua = __builtin_bit_cast(u32x2, a), ub = __builtin_bit_cast(u32x2, b);
+            f.v = u32x4{ua[0], ua[1], ub[0], ub[1]};
+        } else {
+            const int c = 16 * n + i;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int row = 32 * kk + 4 * g + j;
+                f.a[j] = *reinterpret_cast<const float*>(t + at(row, c >> 2) + (c & 3) * 4);
+                f.b[j] = *reinterpret_cast<const float*>(t + at(row + 16, c >> 2) + (c & 3) * 4);
+            }
+        }
+        return f;
+    }
+};
+
+// Four fp32 values to columns c .. c + 3 (c a multiple of 4) of a row, split over N tiles.
+template <typename E, int W, int N>
+__device__ __forceinline__ void put4(char* t, int tile_bytes, int row, int c, const f32x4& x) {
+    if constexpr (sizeof(E) == 2) {
+        f32x4 r = x;
+        char* p = t + Tile<E, W>::at(row, c >> 3) + (c & 4) * 2;
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            const u32x2 w = {pack_bf16(r[0], r[1]), pack_bf16(r[2], r[3])};
+            *reinterpret_cast<u32x2*>(p + n * tile_bytes) = w;
+            if (n + 1 < N) {
+                r[0] -= bf_lo(w[0]);
+                r[1] -= bf_hi(w[0]);
+                r[2] -= bf_lo(w[1]);
+                r[3] -= bf_hi(w[1]);
+            }
+        }
+    } else {
+        *reinterpret_cast<f32x4*>(t + Tile<E, W>::at(row, c >> 2)) = x;
+    }
+}
+
+// ---------------------------------------------------------------- global memory
+// 16-byte pieces of a chunk's rows (W values from column 0 of `base`) held in registers
+// between their load and their store to LDS; rows from `live` on are zero, whatever the
+// memory holds there.
+template <typename E, int W>
+struct Staged {
+    static constexpr int PIECES = GC * Tile<E, W>::NP / THREADS;
+    u32x4 r[PIECES];
+
+    __device__ __forceinline__ void load(const E* base, int64_t stride, int live, int tid) {
+#pragma unroll
+        for (int n = 0; n < PIECES; ++n) {
+            const int p = tid + n * THREADS, row = p / Tile<E, W>::NP, pc = p % Tile<E, W>::NP;
+            r[n] = u32x4{0, 0, 0, 0};
+            if (row < live) r[n] = *reinterpret_cast<const u32x4*>(base + (int64_t)row * stride + pc * (16 / (int)sizeof(E)));
+        }
+    }
+    __device__ __forceinline__ void store(char* t, int tid) const {
+#pragma unroll
+        for (int n = 0; n < PIECES; ++n) {
+            const int p = tid + n * THREADS;
+            *reinterpret_cast<u32x4*>(t + Tile<E, W>::at(p / Tile<E, W>::NP, p % Tile<E, W>::NP)) = r[n];
+        }
+    }
+};
+
+__device__ __forceinline__ void load_row(const uint16_t* p, bool live, Frag<uint16_t>& f) {
+    f.v = u32x4{0, 0, 0, 0};
+    if (live) f.v = *reinterpret_cast<const u32x4*>(p);
+}
+__device__ __forceinline__ void load_row(const float* p, bool live, Frag<float>& f) {
+    f.a = f.b = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (live) {
+        f.a = *reinterpret_cast<const f32x4*>(p);
+        f.b = *reinterpret_cast<const f32x4*>(p + 4);
+    }
+}
+__device__ __forceinline__ f32x4 load4(const uint16_t* p) {
+    const u32x2 w = *reinterpret_cast<const u32x2*>(p);
+    return f32x4{bf_lo(w[0]), bf_hi(w[0]), bf_lo(w[1]), bf_hi(w[1])};
+}
+__device__ __forceinline__ f32x4 load4(const float* p) { return *reinterpret_cast<const f32x4*>(p); }
+__device__ __forceinline__ void store4(uint16_t* p, const f32x4& x) {
+    *reinterpret_cast<u32x2*>(p) = u32x2{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3])};
+}
+__device__ __forceinline__ void store4(float* p, const f32x4& x) { *reinterpret_cast<f32x4*>(p) = x; }
+
+// ---------------------------------------------------------------- gates
+// Running sum of a chunk's gates in powers of two, a token a lane, as a whole part h
+// (exact) and a fraction f in [-1/2, 1/2]: exp(G_t - G_s) = 2^((h_t - h_s) + (f_t - f_s))
+// keeps the precision of its own size however far the sums have run.  A gate below
+// 2^-256 counts as 2^-256, which is 0 in fp32 like itself; so -infinity is a gate of 0.
+struct Gates {
+    float h, f;
+};
+__device__ __forceinline__ Gates gate_sums(float g, int lane) {
+    Gates s;
+    const float x = g * LOG2E;
+    if (x < -256.f) {
+        s.h = -256.f;
+        s.f = 0.f;
+    } else {
+        s.h = rintf(x);
+        s.f = fmaf(g, LOG2E, -s.h) + g * LOG2E_LOW;
+    }
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        const float h = __shfl_up(s.h, o, 64), f = __shfl_up(s.f, o, 64);
+        if (lane >= o) {
+            s.h += h;
+            s.f += f;
+            const float r = rintf(s.f);
+            s.h += r;
+            s.f -= r;
+        }
+    }
+    return s;
+}
+__device__ __forceinline__ float pow2(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// ---------------------------------------------------------------- the state in accumulators
+// Tiles of 16 x 16 of the D x EB state, spread over the four waves: wave w holds the row
+// tiles w, w + 4, .. with all column tiles, or at D = 32 row tile w % 2 and half the columns.
+template <int D, int EB>
+struct StateTiles {
+    static constexpr int CT = D / 16, ET = EB / 16;
+    static constexpr int CW = CT >= 4 ? CT / 4 : 1;
+    static constexpr int EW = CT >= 4 ? ET : ET / 2;
+    typedef f32x4 Acc[CW][EW];
+    __device__ static __forceinline__ int ct(int wave, int n) { return CT >= 4 ? wave + 4 * n : (wave & 1); }
+    __device__ static __forceinline__ int et(int wave, int n) { return CT >= 4 ? n : (wave >> 1) * EW + n; }
+};
+
+// S = decay S + sum_s w_s y_s z_s^T over a chunk's tiles.  The weighted keys enter the
+// matrix cores as fp32 values split into three bf16 terms: the state is an fp32 sum of
+// products rounded as in fp32, which the terms' three products per tile pay for.
+template <typename E, int D, int EB>
+__device__ __forceinline__ void update_state(typename StateTiles<D, EB>::Acc& S, const char* yt,
+                                             const char* zt, const float* w, float decay, int wave, int lane) {
+    using ST = StateTiles<D, EB>;
+    constexpr int N = sizeof(E) == 2 ? 3 : 1;
+#pragma unroll
+    for (int a = 0; a < ST::CW; ++a)
+#pragma unroll
+        for (int b = 0; b < ST::EW; ++b) S[a][b] = S[a][b] * decay;
+#pragma unroll
+    for (int kk = 0; kk < GC / 32; ++kk) {
+        const int g = lane >> 4;
+        const f32x4 w0 = *reinterpret_cast<const f32x4*>(w + 32 * kk + 4 * g);
+        const f32x4 w1 = *reinterpret_cast<const f32x4*>(w + 32 * kk + 16 + 4 * g);
+        Frag<E> ys[ST::CW][N];
+#pragma unroll
+        for (int a = 0; a < ST::CW; ++a) {
+            float x[8];
+            widen(Tile<E, D>::cols(yt, kk, ST::ct(wave, a), lane), x);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                x[j] *= w0[j];
+                x[4 + j] *= w1[j];
+            }
+            split<N>(x, ys[a]);
+        }
+#pragma unroll
+        for (int b = 0; b < ST::EW; ++b) {
+            const Frag<E> z = Tile<E, EB>::cols(zt, kk, ST::et(wave, b), lane);
+#pragma unroll
+            for (int a = 0; a < ST::CW; ++a)
+#pragma unroll
+                for (int n = 0; n < N; ++n) S[a][b] = mma(ys[a][N - 1 - n], z, S[a][b]);
+        }
+    }
+}
+
+// Where a state lies in memory: element (c, e) of the walk at c * sc + e * se.
+template <int D, int EB>
+__device__ __forceinline__ void load_state(typename StateTiles<D, EB>::Acc& S, const float* p,
+                                           int sc, int se, int wave, int lane) {
+    using ST = StateTiles<D, EB>;
+#pragma unroll
+    for (int a = 0; a < ST::CW; ++a)
+#pragma unroll
+        for (int b = 0; b < ST::EW; ++b) {
+            const int c = 16 * ST::ct(wave, a) + 4 * (lane >> 4), e = 16 * ST::et(wave, b) + (lane & 15);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) S[a][b][j] = p ? p[(c + j) * sc + e * se] : 0.f;
+        }
+}
+template <int D, int EB>
+__device__ __forceinline__ void store_state(const typename StateTiles<D, EB>::Acc& S, float* p,
+                                            int sc, int se, int wave, int lane) {
+    using ST = StateTiles<D, EB>;
+#pragma unroll
+    for (int a = 0; a < ST::CW; ++a)
+#pragma unroll
+        for (int b = 0; b < ST::EW; ++b) {
+            const int c = 16 * ST::ct(wave, a) + 4 * (lane >> 4), e = 16 * ST::et(wave, b) + (lane & 15);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) p[(c + j) * sc + e * se] = S[a][b][j];
+        }
+}
+
+// ---------------------------------------------------------------- the walk
+// One role: [B, T, heads, D] with a token stride.
+struct Role {
+    const void* p;
+    int64_t stride;
+};
+
+struct Walk {
+    Role x, y, z, x2;
+    void* out;           // [B, T, HK * nx, D]
+    float* r;            // x2 . out without a token's own term, [blocks][B, T, HK * nx]
+    const float* g;
+    const int32_t* lens;
+    const float* start;  // state before the walk's first chunk
+    int64_t start_pair, start_seg;   // offsets of a (b, kv head) and of a segment
+    float* end;          // state after the sequence, or nullptr
+    int sc, se;          // strides of a state's key-role and value-role index
+    int B, T, HK, nx, ny, nseg, seg_chunks;
+    float pair_scale, row_scale, key_scale;
+};
+
+// A workgroup of four waves walks the chunks of one segment of one (b, kv head), for EB of
+// the value columns.  Wave w has the chunk's tokens 16 w .. 16 w + 15 as rows; products are
+// formed transposed (Y X^T, then Z^T P^T), so that P leaves the accumulators as the next
+// product's operand and a lane stores four neighbouring values of one token.
+// P and S are taken as two bf16 terms (three for the sums r, which are fp32 results), so
+// that the output is rounded once.
+template <typename E, int D, int EB, bool REV, bool DOT>
+__global__ void __launch_bounds__(THREADS) gated_walk(Walk w) {
+    using TY = Tile<E, D>;
+    using TZ = Tile<E, EB>;
+    using ST = StateTiles<D, EB>;
+    constexpr int NS = sizeof(E) == 4 ? 1 : DOT ? 3 : 2;   // terms of S
+    constexpr int NP = sizeof(E) == 4 ? 1 : 2;             // terms of P
+    constexpr int KD = D / 32, KE = EB / 32, ET = EB / 16;
+    constexpr int YB = GC * TY::ROWB, ZB = GC * TZ::ROWB, SB = EB * TY::ROWB;
+    __shared__ __attribute__((aligned(16))) char lds[YB + ZB + NS * SB + 3 * GC * 4];
+    char* yt = lds;
+    char* zt = lds + YB;
+    char* stt = lds + YB + ZB;   // S transposed, [e][c], NS terms
+    float* gh = reinterpret_cast<float*>(lds + YB + ZB + NS * SB);
+    float* gf = gh + GC;
+    float* kw = gf + GC;
+
+    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, li = lane & 15, lg = lane >> 4;
+    constexpr int NB = D / EB;
+    int id = blockIdx.x;
+    const int eb = id % NB;
+    id /= NB;
+    const int seg = id % w.nseg;
+    id /= w.nseg;
+    const int hk = id % w.HK, b = id / w.HK;
+
+    const int T = w.T;
+    int len = T;
+    if (w.lens) len = min(max(w.lens[b], 0), T);
+    const int c0 = seg * w.seg_chunks, c1 = min(c0 + w.seg_chunks, (T + GC - 1) / GC);
+    const int live_end = min(c1, (len + GC - 1) / GC);   // chunks from here on hold no live token
+    const int hx_all = w.HK * w.nx, hy_all = w.HK * w.ny;
+    const int64_t tok0 = (int64_t)b * T;
+    E* const out = static_cast<E*>(w.out);
+
+    typename ST::Acc S;
+    load_state<D, EB>(S, w.start ? w.start + ((int64_t)b * w.HK + hk) * w.start_pair + seg * w.start_seg + eb * EB * w.se : nullptr,
+                      w.sc, w.se, wave, lane);
+
+    // rows of dead chunks are zero
+    {
+        const int t0 = max(c0, live_end) * GC, n = min(c1 * GC, T) - t0;
+        constexpr int PC = EB / 4;
+        const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+        for (int64_t p = tid; p < (int64_t)n * w.nx * PC; p += THREADS) {
+            const int row = (int)(p / (w.nx * PC)), rest = (int)(p % (w.nx * PC));
+            const int64_t tk = tok0 + t0 + row;
+            const int h = hk * w.nx + rest / PC;
+            store4(out + (tk * hx_all + h) * D + eb * EB + (rest % PC) * 4, zero);
+            if (DOT && rest % PC == 0) w.r[((int64_t)eb * w.B * T + tk) * hx_all + h] = 0.f;
+        }
+    }
+
+    const int items = max(live_end - c0, 0) * w.ny;
+    Staged<E, D> ys;
+    Staged<E, EB> zs;
+    float graw = 0.f;
+    auto fetch = [&](int it) {
+        const int ci = it / w.ny, hy = it - ci * w.ny;
+        const int c = REV ? live_end - 1 - ci : c0 + ci;
+        const int live = min(len - c * GC, GC);
+        const int64_t tk = tok0 + (int64_t)c * GC;
+        const int h = hk * w.ny + hy;
+        ys.load(static_cast<const E*>(w.y.p) + tk * w.y.stride + h * D, w.y.stride, live, tid);
+        zs.load(static_cast<const E*>(w.z.p) + tk * w.z.stride + h * D + eb * EB, w.z.stride, live, tid);
+        if (hy == 0) graw = lane < live ? w.g[(tk + lane) * w.HK + hk] : 0.f;
+    };
+    if (items > 0) fetch(0);
+
+    f32x4 o[ET];
+    float rsum = 0.f;
+    Gates gs = {0.f, 0.f};
+    float eh = 0.f, ef = 0.f;
+    for (int it = 0; it < items; ++it) {
+        const int ci = it / w.ny, hy = it - ci * w.ny;
+        const int c = REV ? live_end - 1 - ci : c0 + ci;
+        const int t = c * GC + 16 * wave + li;    // this lane's token
+        const bool live = t < len;
+        __syncthreads();                          // the last item's reads are over
+        ys.store(yt, tid);
+        zs.store(zt, tid);
+        if (hy == 0) {
+            gs = gate_sums(graw, lane);
+            eh = __shfl(gs.h, 63, 64);
+            ef = __shfl(gs.f, 63, 64);
+            if (wave == 0) {
+                gh[lane] = gs.h;
+                gf[lane] = gs.f;
+                kw[lane] = w.key_scale * (REV ? pow2(gs.h + gs.f) : pow2((eh - gs.h) + (ef - gs.f)));
+            }
+#pragma unroll
+            for (int a = 0; a < ST::CW; ++a)
+#pragma unroll
+                for (int e = 0; e < ST::EW; ++e)
+                    put4<E, D, NS>(stt, SB, 16 * ST::et(wave, e) + li, 16 * ST::ct(wave, a) + 4 * lg, S[a][e]);
+        }
+        __syncthreads();
+        if (it + 1 < items) fetch(it + 1);
+
+        const float th = gh[16 * wave + li], tf = gf[16 * wave + li];
+        for (int hx = 0; hx < w.nx; ++hx) {
+            const int h = hk * w.nx + hx;
+            const int64_t tk = tok0 + t;
+            Frag<E> xf[KD];
+#pragma unroll
+            for (int kk = 0; kk < KD; ++kk)
+                load_row(static_cast<const E*>(w.x.p) + tk * w.x.stride + h * D + 32 * kk + 8 * lg, live, xf[kk]);
+            Frag<E> x2f[DOT ? KE : 1];
+            const E* x2 = DOT ? static_cast<const E*>(w.x2.p) + tk * w.x2.stride + h * D + eb * EB : nullptr;
+            if constexpr (DOT) {
+#pragma unroll
+                for (int kk = 0; kk < KE; ++kk) load_row(x2 + 32 * kk + 8 * lg, live, x2f[kk]);
+            }
+            if (hy == 0) {
+                // from the state: o = S^T x
+                const float rf = w.row_scale * (REV ? pow2((eh - th) + (ef - tf)) : pow2(th + tf));
+                rsum = 0.f;
+#pragma unroll
+                for (int e = 0; e < ET; ++e) {
+                    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int n = NS - 1; n >= 0; --n)
+#pragma unroll
+                        for (int kk = 0; kk < KD; ++kk)
+                            acc = mma(TY::rows(stt + n * SB, 16 * e, kk, lane), xf[kk], acc);
+                    o[e] = acc * rf;
+                    if constexpr (DOT) {
+                        f32x4 u = {0.f, 0.f, 0.f, 0.f};
+                        if (live) u = load4(x2 + 16 * e + 4 * lg);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) rsum += u[j] * o[e][j];
+                    }
+                }
+            }
+            // from the chunk: 32 tokens s at a time, those that some row of the wave sees
+#pragma unroll
+            for (int kk = 0; kk < GC / 32; ++kk) {
+                if (REV ? 2 * kk + 1 < wave : 2 * kk > wave) continue;
+                float p[8];
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const int st = 2 * kk + u;
+                    f32x4 acc = {0.f, 0.f, 0.f, 0.f}, m = {0.f, 0.f, 0.f, 0.f};
+                    if (REV ? st >= wave : st <= wave) {
+#pragma unroll
+                        for (int k = 0; k < KD; ++k) acc = mma(TY::rows(yt, 16 * st, k, lane), xf[k], acc);
+                        if constexpr (DOT) {
+#pragma unroll
+                            for (int k = 0; k < KE; ++k) m = mma(TZ::rows(zt, 16 * st, k, lane), x2f[k], m);
+                        }
+                    }
+                    const f32x4 sh = *reinterpret_cast<const f32x4*>(gh + 16 * st + 4 * lg);
+                    const f32x4 sf = *reinterpret_cast<const f32x4*>(gf + 16 * st + 4 * lg);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int s = 16 * st + 4 * lg + j, tt = 16 * wave + li;
+                        const float d = (th - sh[j]) + (tf - sf[j]);
+                        const float dec = w.pair_scale * pow2(REV ? -d : d);
+                        const bool sees = REV ? s >= tt : s <= tt;
+                        const float v = sees ? acc[j] * dec : 0.f;
+                        p[4 * u + j] = v;
+                        if constexpr (DOT) rsum += sees && s != tt ? v * m[j] : 0.f;
+                    }
+                }
+                Frag<E> pf[NP];
+                split<NP>(p, pf);
+#pragma unroll
+                for (int e = 0; e < ET; ++e) {
+                    const Frag<E> z = TZ::cols(zt, kk, e, lane);
+#pragma unroll
+                    for (int n = NP - 1; n >= 0; --n) o[e] = mma(z, pf[n], o[e]);
+                }
+            }
+            if (hy == w.ny - 1) {
+                if (t < T) {
+                    const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int e = 0; e < ET; ++e)
+                        store4(out + (tk * hx_all + h) * D + eb * EB + 16 * e + 4 * lg, live ? o[e] : zero);
+                }
+                if constexpr (DOT) {
+                    float s = rsum + shfl_xor(rsum, 16);
+                    s += shfl_xor(s, 32);
+                    if (lg == 0 && t < T) w.r[((int64_t)eb * w.B * T + tk) * hx_all + h] = live ? s : 0.f;
+                }
+            }
+        }
+        update_state<E, D, EB>(S, yt, zt, kw, hy == 0 ? pow2(eh + ef) : 1.f, wave, lane);
+    }
+    if (w.end && (REV ? seg == 0 : seg == w.nseg - 1))
+        store_state<D, EB>(S, w.end + ((int64_t)b * w.HK + hk) * D * D + eb * EB * w.se, w.sc, w.se, wave, lane);
+    (void)hy_all;
+}
+
+// ---------------------------------------------------------------- segments
+// What each segment adds to the state, from zero, for the forward state (Y = k, Z = v) and,
+// with two roles, for the backward one (Y = q, Z = do of all the group's heads), and the
+// segment's decay.
+struct Local {
+    Role y[2], z[2];
+    int ny[2];
+    float* st[2];
+    int64_t pair[2], first[2];   // offset of a (b, kv head); of segment 0's place in it
+    float key_scale[2];
+    int roles;
+    float* dec;
+    const float* g;
+    const int32_t* lens;
+    int B, T, HK, nseg, seg_chunks;
+};
+
+template <typename E, int D, int EB>
+__global__ void __launch_bounds__(THREADS) gated_local(Local w) {
+    using TY = Tile<E, D>;
+    using TZ = Tile<E, EB>;
+    using ST = StateTiles<D, EB>;
+    constexpr int YB = GC * TY::ROWB, ZB = GC * TZ::ROWB;
+    __shared__ __attribute__((aligned(16))) char lds[YB + ZB + GC * 4];
+    char* yt = lds;
+    char* zt = lds + YB;
+    float* kw = reinterpret_cast<float*>(lds + YB + ZB);
+    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+    constexpr int NB = D / EB;
+    int id = blockIdx.x;
+    const int eb = id % NB;
+    id /= NB;
+    const int role = id % w.roles;
+    id /= w.roles;
+    const int seg = id % w.nseg;
+    id /= w.nseg;
+    const int hk = id % w.HK, b = id / w.HK;
+    const int T = w.T;
+    int len = T;
+    if (w.lens) len = min(max(w.lens[b], 0), T);
+    const int c0 = seg * w.seg_chunks, c1 = min(c0 + w.seg_chunks, (T + GC - 1) / GC);
+    const int live_end = min(c1, (len + GC - 1) / GC);
+    const int ny = role ? w.ny[1] : w.ny[0];
+    const Role ry = role ? w.y[1] : w.y[0], rz = role ? w.z[1] : w.z[0];
+    const float key_scale = role ? w.key_scale[1] : w.key_scale[0];
+    const int64_t tok0 = (int64_t)b * T;
+
+    const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+    typename ST::Acc S;
+#pragma unroll
+    for (int a = 0; a < ST::CW; ++a)
+#pragma unroll
+        for (int e = 0; e < ST::EW; ++e) S[a][e] = zero;
+    float dec = 1.f;
+
+    const int items = max(live_end - c0, 0) * ny;
+    Staged<E, D> ys;
+    Staged<E, EB> zs;
+    float graw = 0.f;
+    auto fetch = [&](int it) {
+        const int ci = it / ny, hy = it - ci * ny;
+        const int c = role ? live_end - 1 - ci : c0 + ci;
+        const int live = min(len - c * GC, GC);
+        const int64_t tk = tok0 + (int64_t)c * GC;
+        const int h = hk * ny + hy;
+        ys.load(static_cast<const E*>(ry.p) + tk * ry.stride + h * D, ry.stride, live, tid);
+        zs.load(static_cast<const E*>(rz.p) + tk * rz.stride + h * D + eb * EB, rz.stride, live, tid);
+        if (hy == 0) graw = lane < live ? w.g[(tk + lane) * w.HK + hk] : 0.f;
+    };
+    if (items > 0) fetch(0);
+    float decay = 1.f;
+    for (int it = 0; it < items; ++it) {
+        const int hy = it % ny;
+        __syncthreads();
+        ys.store(yt, tid);
+        zs.store(zt, tid);
+        decay = 1.f;
+        if (hy == 0) {
+            const Gates gs = gate_sums(graw, lane);
+            const float eh = __shfl(gs.h, 63, 64), ef = __shfl(gs.f, 63, 64);
+            if (wave == 0) kw[lane] = key_scale * (role ? pow2(gs.h + gs.f) : pow2((eh - gs.h) + (ef - gs.f)));
+            decay = pow2(eh + ef);
+            dec *= decay;
+        }
+        __syncthreads();
+        if (it + 1 < items) fetch(it + 1);
+        update_state<E, D, EB>(S, yt, zt, kw, decay, wave, lane);
+    }
+    const int64_t pair = (int64_t)b * w.HK + hk;
+    float* st = (role ? w.st[1] : w.st[0]) + pair * (role ? w.pair[1] : w.pair[0]) + (role ? w.first[1] : w.first[0]) +
+                (int64_t)seg * D * D;
+    store_state<D, EB>(S, st + eb * EB, D, 1, wave, lane);
+    if (tid == 0 && eb == 0 && role == 0) w.dec[pair * w.nseg + seg] = dec;
+}
+
+// Joins the segments: fst[j] becomes the state before segment j (j = nseg: after the last),
+// rst[j] the gradient of the state after segment j.  A thread has one element of one pair's
+// states; the segments' values and decays do not depend on each other's, so their loads run
+// ahead of the sums.
+__global__ void __launch_bounds__(THREADS) gated_join(float* fst, const float* s0, float* rst, const float* ds1,
+                                                      const float* dec, int nseg, int DD) {
+    const int64_t pair = blockIdx.y;
+    const int i = blockIdx.x * THREADS + threadIdx.x;
+    const float* d = dec + pair * nseg;
+    if (i < DD) {
+        float* p = fst + pair * (nseg + 1) * DD + i;
+        float s = s0 ? s0[pair * DD + i] : 0.f;
+        p[0] = s;
+        for (int j0 = 0; j0 < nseg; j0 += 8) {
+            float loc[8], a[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const int j = min(j0 + u, nseg - 1);
+                loc[u] = p[(int64_t)(j + 1) * DD];
+                a[u] = d[j];
+            }
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+                if (j0 + u < nseg) {
+                    s = a[u] * s + loc[u];
+                    p[(int64_t)(j0 + u + 1) * DD] = s;
+                }
+        }
+    } else if (rst && i < 2 * DD) {
+        const int e = i - DD;
+        float* p = rst + pair * nseg * DD + e;
+        float s = ds1 ? ds1[pair * DD + e] : 0.f;
+        // segment j's own sum lies at j; the state's gradient behind segment j replaces it
+        for (int j0 = nseg - 1; j0 >= 0; j0 -= 8) {
+            float loc[8], a[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const int j = max(j0 - u, 0);
+                loc[u] = p[(int64_t)j * DD];
+                a[u] = d[j];
+            }
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+                if (j0 - u >= 0) {
+                    p[(int64_t)(j0 - u) * DD] = s;
+                    s = a[u] * s + loc[u];
+                }
+        }
+    }
+}
+
+// ---------------------------------------------------------------- gradient of the gates
+// dg_t sums the products of pairs s < t <= t', which is
+//   sum_{t' >= t} q_t' . dq_t' - sum_{s >= t} k_s . dk_s + <S, dL/dS> at the segment's end
+// (a token's product with itself left out of both sums, where it would only cancel).  A
+// workgroup takes one segment of one (b, kv head), 256 tokens at a time from the last; the
+// sums run in 64 bits, since they cancel.  A gate of 0 passes no gradient.
+struct GateGrad {
+    const float* rq;
+    const float* rk;
+    const float* fst;
+    const float* rst;
+    const float* g;
+    const int32_t* lens;
+    float* dg;
+    int B, T, HK, nx, nb, nseg, seg_chunks, DD;
+};
+__global__ void __launch_bounds__(THREADS) gated_gate_grad(GateGrad w) {
+    __shared__ double part[4];
+    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+    int id = blockIdx.x;
+    const int seg = id % w.nseg;
+    id /= w.nseg;
+    const int hk = id % w.HK, b = id / w.HK;
+    const int64_t pair = (int64_t)b * w.HK + hk;
+    const int T = w.T;
+    int len = T;
+    if (w.lens) len = min(max(w.lens[b], 0), T);
+    const int t0 = seg * w.seg_chunks * GC, t1 = min(t0 + w.seg_chunks * GC, T), live = min(t1, len);
+    const float* S = w.fst + (pair * (w.nseg + 1) + seg + 1) * w.DD;
+    const float* R = w.rst + (pair * w.nseg + seg) * w.DD;
+    double x = 0.0;
+    for (int i = tid; i < w.DD; i += THREADS) x += (double)S[i] * (double)R[i];
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) x += __shfl_xor(x, o, 64);
+    if (lane == 0) part[wave] = x;
+    __syncthreads();
+    double carry = part[0] + part[1] + part[2] + part[3];
+    const int64_t tok0 = (int64_t)b * T;
+    for (int t = live + tid; t < t1; t += THREADS)
+        if (t >= t0) w.dg[(tok0 + t) * w.HK + hk] = 0.f;
+    for (int hi = live; hi > t0; hi -= THREADS) {
+        const int t = hi - 1 - tid;       // descending: thread 0 has the last token
+        double v = 0.0;
+        if (t >= t0) {
+            const int64_t n = (int64_t)w.B * T, tk = tok0 + t;
+            for (int e = 0; e < w.nb; ++e) {
+                for (int h = 0; h < w.nx; ++h) v += (double)w.rq[((e * n + tk) * w.HK + hk) * w.nx + h];
+                v -= (double)w.rk[(e * n + tk) * w.HK + hk];
+            }
+        }
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+            const double u = __shfl_up(v, o, 64);
+            if (lane >= o) v += u;
+        }
+        __syncthreads();                  // part is free
+        if (lane == 63) part[wave] = v;
+        __syncthreads();
+        double before = carry;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            before += k < wave ? part[k] : 0.0;
+            carry += part[k];
+        }
+        if (t >= t0) {
+            const float gate = w.g[(tok0 + t) * w.HK + hk];
+            w.dg[(tok0 + t) * w.HK + hk] = gate < -104.f ? 0.f : (float)(before + v);
+        }
+    }
+}
+
+// ---------------------------------------------------------------- one token
+// S' = exp(g) S + k v^T in place, o = scale S'^T q.  Bound by the state's bytes: read and
+// written once.  A workgroup has EB value columns of one (row, kv head): a thread four
+// columns of every RG-th key row, sixteen bytes a load, the whole state's share in registers.
+// Rows that name the same slot are that sequence's next tokens, in the order of the rows:
+// the first of them does them all, the others leave.
+template <typename E, int D, int EB>
+__global__ void __launch_bounds__(THREADS) gated_step(GatedStep w) {
+    constexpr int CL = EB / 4, RG = THREADS / CL, R = D / RG;   // lanes of a row, row groups, rows of a thread
+    static_assert(CL <= 64 && R >= 1, "a row of columns lies in one wave");
+    __shared__ float part[4][EB];
+    __shared__ int s_next[4];
+    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, cl = tid % CL, rg = tid / CL;
+    constexpr int NB = D / EB;
+    int id = blockIdx.x;
+    const int eb = id % NB;
+    id /= NB;
+    const int hk = id % w.HK, row0 = id / w.HK;
+    const int G = w.H / w.HK, e0 = eb * EB + 4 * cl;
+    const E* const q = static_cast<const E*>(w.q);
+    const E* const k = static_cast<const E*>(w.k);
+    const E* const v = static_cast<const E*>(w.v);
+    E* const out = static_cast<E*>(w.out);
+
+    const int slot = w.slots ? w.slots[row0] : row0;
+    if (slot < 0 || slot >= w.nslots) {       // no sequence: the output is zero
+        const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+        for (int p = tid; p < G * CL; p += THREADS)
+            store4(out + ((int64_t)row0 * w.H + hk * G + p / CL) * D + eb * EB + 4 * (p % CL), zero);
+        return;
+    }
+    float* const st = w.state + ((int64_t)slot * w.HK + hk) * D * D + e0;
+    f32x4 S[R];
+#pragma unroll
+    for (int n = 0; n < R; ++n) S[n] = *reinterpret_cast<const f32x4*>(st + (int64_t)(rg + n * RG) * D);
+
+    // the next row after `row` of the same slot (B if there is none); a row before row0 gives -1
+    auto next_row = [&](int row, bool look_back) {
+        int found = w.B;
+        for (int i0 = look_back ? 0 : (row + 1) / THREADS * THREADS; i0 < w.B; i0 += THREADS) {
+            const int i = i0 + tid;
+            const bool same = i < w.B && i != row && (look_back || i > row) && w.slots[i] == slot;
+            const unsigned long long m = __ballot(same);
+            __syncthreads();
+            if (lane == 0) s_next[wave] = m ? i0 + 64 * wave + __ffsll(m) - 1 : w.B;
+            __syncthreads();
+            found = min(min(s_next[0], s_next[1]), min(s_next[2], s_next[3]));
+            if (found < w.B) break;
+        }
+        return found;
+    };
+    int next = w.B;
+    if (w.slots) {
+        next = next_row(row0, true);
+        if (next < row0) return;              // an earlier row does this one
+    }
+    for (int row = row0; row < w.B; row = next, next = w.slots && row < w.B ? next_row(row, false) : w.B) {
+        const E* kr = k + row * w.ks + (int64_t)hk * D;
+        const f32x4 vv = load4(v + row * w.vs + (int64_t)hk * D + e0);
+        const float g = w.g[(int64_t)row * w.HK + hk];
+        const float a = expf(g);
+#pragma unroll
+        for (int n = 0; n < R; ++n) {
+            float kc;
+            if constexpr (sizeof(E) == 2) kc = bf_lo(kr[rg + n * RG]); else kc = kr[rg + n * RG];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) S[n][j] = fmaf(kc, vv[j], a * S[n][j]);
+        }
+        for (int h = 0; h < G; ++h) {
+            const E* qr = q + row * w.qs + (int64_t)(hk * G + h) * D;
+            f32x4 o = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int n = 0; n < R; ++n) {
+                float qc;
+                if constexpr (sizeof(E) == 2) qc = bf_lo(qr[rg + n * RG]); else qc = qr[rg + n * RG];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) o[j] = fmaf(qc, S[n][j], o[j]);
+            }
+#pragma unroll
+            for (int m = CL; m < 64; m <<= 1)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) o[j] += shfl_xor(o[j], m);
+            __syncthreads();
+            if (lane < CL) *reinterpret_cast<f32x4*>(&part[wave][4 * lane]) = o;
+            __syncthreads();
+            if (tid < CL) {
+                f32x4 s;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    s[j] = w.scale * ((part[0][4 * tid + j] + part[1][4 * tid + j]) + (part[2][4 * tid + j] + part[3][4 * tid + j]));
+                store4(out + ((int64_t)row * w.H + hk * G + h) * D + eb * EB + 4 * tid, s);
+            }
+        }
+    }
+#pragma unroll
+    for (int n = 0; n < R; ++n) *reinterpret_cast<f32x4*>(st + (int64_t)(rg + n * RG) * D) = S[n];
+}
+
+// ---------------------------------------------------------------- launches
+template <typename E, int D, bool REV, bool DOT>
+hipError_t launch_walk(const Walk& w, hipStream_t stream) {
+    constexpr int EB = D < 64 ? D : 64;
+    const int64_t n = (int64_t)w.B * w.HK * w.nseg * (D / EB);
+    gated_walk<E, D, EB, REV, DOT><<<dim3((unsigned)n), THREADS, 0, stream>>>(w);
+    return hipGetLastError();
+}
+
+template <typename E, int D>
+hipError_t launch_local(const Local& w, hipStream_t stream) {
+    constexpr int EB = D < 64 ? D : 64;
+    const int64_t n = (int64_t)w.B * w.HK * w.nseg * w.roles * (D / EB);
+    gated_local<E, D, EB><<<dim3((unsigned)n), THREADS, 0, stream>>>(w);
+    return hipGetLastError();
+}
+
+hipError_t launch_join(float* fst, const float* s0, float* rst, const float* ds1, const float* dec, int pairs, int nseg,
+                       int DD, hipStream_t stream) {
+    const int n = DD * (rst ? 2 : 1);
+    // grid.y is at most 65535: pairs are taken in runs
+    for (int p = 0; p < pairs; p += 65535) {
+        const int64_t o = p;
+        const int m = pairs - p < 65535 ? pairs - p : 65535;
+        gated_join<<<dim3((n + THREADS - 1) / THREADS, m), THREADS, 0, stream>>>(
+            fst + o * (nseg + 1) * DD, s0 ? s0 + o * DD : nullptr, rst ? rst + o * nseg * DD : nullptr,
+            ds1 ? ds1 + o * DD : nullptr, dec + o * nseg, nseg, DD);
+    }
+    return hipGetLastError();
+}
+
+template <typename E, int D>
+hipError_t forward(const GatedForward& f) {
+    const GatedProblem& p = f.p;
+    hipError_t err = hipSuccess;
+    if (p.nseg > 1) {
+        Local l = {};
+        l.roles = 1;
+        l.y[0] = {p.k, p.ks};
+        l.z[0] = {p.v, p.vs};
+        l.ny[0] = 1;
+        l.st[0] = f.fst;
+        l.pair[0] = (int64_t)(p.nseg + 1) * D * D;
+        l.first[0] = D * D;
+        l.key_scale[0] = 1.f;
+        l.dec = f.fdec;
+        l.g = p.g;
+        l.lens = p.lens;
+        l.B = p.B; l.T = p.T; l.HK = p.HK; l.nseg = p.nseg; l.seg_chunks = p.seg_chunks;
+        if ((err = launch_local<E, D>(l, p.stream)) != hipSuccess) return err;
+        if ((err = launch_join(f.fst, p.s0, nullptr, nullptr, f.fdec, p.B * p.HK, p.nseg, D * D, p.stream)) != hipSuccess)
+            return err;
+    }
+    Walk w = {};
+    w.x = {p.q, p.qs};
+    w.y = {p.k, p.ks};
+    w.z = {p.v, p.vs};
+    w.out = f.out;
+    w.g = p.g;
+    w.lens = p.lens;
+    w.start = p.nseg > 1 ? f.fst : p.s0;
+    w.start_pair = p.nseg > 1 ? (int64_t)(p.nseg + 1) * D * D : D * D;
+    w.start_seg = D * D;
+    w.end = f.s1;
+    w.sc = D; w.se = 1;
+    w.B = p.B; w.T = p.T; w.HK = p.HK; w.nx = p.H / p.HK; w.ny = 1; w.nseg = p.nseg; w.seg_chunks = p.seg_chunks;
+    w.pair_scale = w.row_scale = p.scale;
+    w.key_scale = 1.f;
+    return launch_walk<E, D, false, false>(w, p.stream);
+}
+
+template <typename E, int D>
+hipError_t backward(const GatedBackward& f) {
+    const GatedProblem& p = f.p;
+    const int G = p.H / p.HK, DD = D * D;
+    const int64_t hs = (int64_t)p.H * D;
+    hipError_t err;
+    Local l = {};
+    l.roles = 2;
+    l.y[0] = {p.k, p.ks};
+    l.z[0] = {p.v, p.vs};
+    l.y[1] = {p.q, p.qs};
+    l.z[1] = {f.dout, hs};
+    l.ny[0] = 1;
+    l.ny[1] = G;
+    l.st[0] = f.fst;
+    l.st[1] = f.rst;
+    l.pair[0] = (int64_t)(p.nseg + 1) * DD;
+    l.pair[1] = (int64_t)p.nseg * DD;
+    l.first[0] = DD;
+    l.key_scale[0] = 1.f;
+    l.key_scale[1] = p.scale;
+    l.dec = f.fdec;
+    l.g = p.g;
+    l.lens = p.lens;
+    l.B = p.B; l.T = p.T; l.HK = p.HK; l.nseg = p.nseg; l.seg_chunks = p.seg_chunks;
+    if ((err = launch_local<E, D>(l, p.stream)) != hipSuccess) return err;
+    if ((err = launch_join(f.fst, p.s0, f.rst, f.ds1, f.fdec, p.B * p.HK, p.nseg, DD, p.stream)) != hipSuccess) return err;
+
+    Walk w = {};
+    w.g = p.g;
+    w.lens = p.lens;
+    w.B = p.B; w.T = p.T; w.HK = p.HK; w.nseg = p.nseg; w.seg_chunks = p.seg_chunks;
+    w.start_seg = DD;
+    // dq and q . dq
+    w.x = {f.dout, hs};
+    w.y = {p.v, p.vs};
+    w.z = {p.k, p.ks};
+    w.x2 = {p.q, p.qs};
+    w.out = f.dq;
+    w.r = f.rq;
+    w.start = f.fst;
+    w.start_pair = (int64_t)(p.nseg + 1) * DD;
+    w.sc = 1; w.se = D;
+    w.nx = G; w.ny = 1;
+    w.pair_scale = w.row_scale = p.scale;
+    w.key_scale = 1.f;
+    if ((err = launch_walk<E, D, false, true>(w, p.stream)) != hipSuccess) return err;
+    // dv, and the initial state's gradient
+    w.x = {p.k, p.ks};
+    w.y = {p.q, p.qs};
+    w.z = {f.dout, hs};
+    w.x2 = {nullptr, 0};
+    w.out = f.dv;
+    w.r = nullptr;
+    w.start = f.rst;
+    w.start_pair = (int64_t)p.nseg * DD;
+    w.end = f.ds0;
+    w.sc = D; w.se = 1;
+    w.nx = 1; w.ny = G;
+    w.row_scale = 1.f;
+    w.key_scale = p.scale;
+    if ((err = launch_walk<E, D, true, false>(w, p.stream)) != hipSuccess) return err;
+    // dk and k . dk
+    w.x = {p.v, p.vs};
+    w.y = {f.dout, hs};
+    w.z = {p.q, p.qs};
+    w.x2 = {p.k, p.ks};
+    w.out = f.dk;
+    w.r = f.rk;
+    w.end = nullptr;
+    w.sc = 1; w.se = D;
+    if ((err = launch_walk<E, D, true, true>(w, p.stream)) != hipSuccess) return err;
+
+    GateGrad d;
+    d.rq = f.rq; d.rk = f.rk; d.fst = f.fst; d.rst = f.rst; d.g = p.g; d.lens = p.lens; d.dg = f.dg;
+    d.B = p.B; d.T = p.T; d.HK = p.HK; d.nx = G; d.nb = gated_value_blocks(D); d.nseg = p.nseg;
+    d.seg_chunks = p.seg_chunks; d.DD = DD;
+    gated_gate_grad<<<dim3((unsigned)((int64_t)p.B * p.HK * p.nseg)), THREADS, 0, p.stream>>>(d);
+    return hipGetLastError();
+}
+
+template <typename E, int D>
+hipError_t step(const GatedStep& s) {
+    constexpr int EB = D < 64 ? D : 64;
+    gated_step<E, D, EB><<<dim3((unsigned)((int64_t)s.B * s.HK * (D / EB))), THREADS, 0, s.stream>>>(s);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t run_gated_forward(const GatedForward& f) {
+    if (f.p.bf16)
+        return f.p.D == 32 ? forward<uint16_t, 32>(f) : f.p.D == 64 ? forward<uint16_t, 64>(f) : forward<uint16_t, 128>(f);
+    return f.p.D == 32 ? forward<float, 32>(f) : f.p.D == 64 ? forward<float, 64>(f) : forward<float, 128>(f);
+}
+
+hipError_t run_gated_backward(const GatedBackward& f) {
+    if (f.p.bf16)
+        return f.p.D == 32 ? backward<uint16_t, 32>(f) : f.p.D == 64 ? backward<uint16_t, 64>(f) : backward<uint16_t, 128>(f);
+    return f.p.D == 32 ? backward<float, 32>(f) : f.p.D == 64 ? backward<float, 64>(f) : backward<float, 128>(f);
+}
+
+hipError_t run_gated_step(const GatedStep& s) {
+    if (s.bf16) return s.D == 32 ? step<uint16_t, 32>(s) : s.D == 64 ? step<uint16_t, 64>(s) : step<uint16_t, 128>(s);
+    return s.D == 32 ? step<float, 32>(s) : s.D == 64 ? step<float, 64>(s) : step<float, 128>(s);
+}
+
+}  // namespace mhla

@@ -13,6 +13,7 @@
 #include <cstring>
 #include <mutex>
 
+#include "gated.h"
 #include "launch.h"
 
 namespace {
@@ -872,6 +873,394 @@ mhla_status stream_impl(const void* q, const void* k, const void* v, const float
     if (owned) (void)hipFreeAsync(ws, stream);
     return err == hipSuccess ? MHLA_OK : MHLA_ERR_HIP;
 }
+
+// ---------------------------------------------------------------- sequences: gated attention, q/k norm and rotation
+
+struct Seq {
+    int64_t B, T, H, HK, D;
+    int64_t qs, ks, vs;
+    size_t esz;
+    int64_t tokens() const { return B * T; }
+    bool empty() const { return B == 0 || H == 0 || HK == 0; }
+    // bytes from a strided tensor's first value past its last one; 0 without tokens
+    size_t span(int64_t heads, int64_t stride) const {
+        return tokens() == 0 ? 0 : (size_t)((tokens() - 1) * stride + heads * D) * esz;
+    }
+    size_t rows(int64_t heads) const { return (size_t)(tokens() * heads * D) * esz; }
+    size_t states() const { return (size_t)(B * HK * D * D) * 4; }
+};
+
+// groups: whether heads have to be a multiple of kv_heads
+mhla_status check_seq(const mhla_seq* q, Seq* s, bool groups) {
+    if (!q) return MHLA_ERR_INVALID_ARG;
+    if (q->dtype != MHLA_F32 && q->dtype != MHLA_BF16) return MHLA_ERR_UNSUPPORTED;
+    if (q->head_dim != 32 && q->head_dim != 64 && q->head_dim != 128) return MHLA_ERR_UNSUPPORTED;
+    if (q->batch < 0 || q->tokens < 0 || q->heads < 0 || q->kv_heads < 0) return MHLA_ERR_INVALID_ARG;
+    if (q->tokens > (1 << 30) || q->heads > 65536 || q->kv_heads > 65536) return MHLA_ERR_UNSUPPORTED;
+    if (groups && (q->kv_heads == 0 ? q->heads != 0 : q->heads % q->kv_heads != 0)) return MHLA_ERR_INVALID_ARG;
+    if (!std::isfinite(q->scale)) return MHLA_ERR_INVALID_ARG;
+    s->B = q->batch; s->T = q->tokens; s->H = q->heads; s->HK = q->kv_heads; s->D = q->head_dim;
+    s->esz = q->dtype == MHLA_F32 ? 4 : 2;
+    const int64_t in[3] = {q->q_stride, q->k_stride, q->v_stride};
+    const int64_t least[3] = {s->H * s->D, s->HK * s->D, s->HK * s->D};
+    int64_t* const out[3] = {&s->qs, &s->ks, &s->vs};
+    for (int i = 0; i < 3; ++i) {
+        *out[i] = in[i] == 0 ? least[i] : in[i];
+        if (*out[i] < least[i]) return MHLA_ERR_INVALID_ARG;
+        if (*out[i] * (int64_t)s->esz % 16 != 0) return MHLA_ERR_MISALIGNED;
+        if (*out[i] > ((int64_t)1 << 40)) return MHLA_ERR_UNSUPPORTED;
+        // every tensor's bytes stay within 2^62
+        if ((double)s->B * (double)s->T * (double)*out[i] * 4.0 > 4.6e18) return MHLA_ERR_UNSUPPORTED;
+    }
+    return MHLA_OK;
+}
+
+// Segments of a sequence: workgroups walk them side by side.  One more segment costs a pass
+// over its keys and values and a state written and read, so a sequence is split only while
+// there are fewer than WALKS walks, and not into segments of fewer than LEAST chunks.
+// Backwards, segments of at most MOST chunks: the gates' gradients start anew from <S, dS>
+// at each segment's end.
+struct GatedPlan {
+    int nseg, seg_chunks;
+    size_t fst, rst, dec, rq, rk, total;
+};
+GatedPlan gated_plan(const Seq& s, bool backward) {
+    constexpr int64_t WALKS = 1024, LEAST = 4, MOST = 16;
+    const int64_t C = mhla::GATED_CHUNK, chunks = s.T > 0 ? (s.T + C - 1) / C : 1;
+    const int64_t walks = s.B * s.HK * mhla::gated_value_blocks((int)s.D);
+    int64_t n = (WALKS + walks - 1) / walks;
+    if (n > (chunks + LEAST - 1) / LEAST) n = (chunks + LEAST - 1) / LEAST;
+    if (backward && n < (chunks + MOST - 1) / MOST) n = (chunks + MOST - 1) / MOST;
+    if (n < 1) n = 1;
+    GatedPlan p;
+    p.seg_chunks = (int)((chunks + n - 1) / n);
+    p.nseg = (int)((chunks + p.seg_chunks - 1) / p.seg_chunks);
+    const size_t pairs = (size_t)(s.B * s.HK), state = (size_t)(s.D * s.D) * 4;
+    const size_t nb = (size_t)mhla::gated_value_blocks((int)s.D);
+    p.fst = 0;
+    p.dec = p.fst + align_up(pairs * (size_t)(p.nseg + 1) * state);
+    p.rst = p.dec + align_up(pairs * (size_t)p.nseg * 4);
+    if (!backward) {
+        p.rq = p.rk = p.rst;
+        p.total = p.nseg > 1 ? p.rst : 0;
+        return p;
+    }
+    p.rq = p.rst + align_up(pairs * (size_t)p.nseg * state);
+    p.rk = p.rq + align_up(nb * (size_t)(s.tokens() * s.H) * 4);
+    p.total = p.rk + align_up(nb * (size_t)(s.tokens() * s.HK) * 4);
+    return p;
+}
+
+mhla_status check_gated(const mhla_seq* seq, Seq* s) {
+    const mhla_status st = check_seq(seq, s, true);
+    if (st != MHLA_OK) return st;
+    if (s->empty()) return MHLA_OK;
+    // workgroups of a launch: two roles of a segment's value blocks at most
+    const double walks = (double)s->B * (double)s->HK * mhla::gated_value_blocks((int)s->D);
+    const double segs = (double)s->T / mhla::GATED_CHUNK + 1;
+    if (walks >= 1073741824.0 || walks * segs * 2 >= 2147483648.0) return MHLA_ERR_UNSUPPORTED;
+    return MHLA_OK;
+}
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+struct Span {
+    const void* p;
+    size_t n;
+};
+
+// Outputs against inputs, each other and the workspace.  `same`: pairs (output, input) that may
+// be one tensor.  Null pointers and empty spans overlap nothing.
+bool spans_clash(const Span* in, int ni, const Span* out, int no, const void* ws, size_t need, const int (*same)[2],
+                 int ns) {
+    auto hit = [](const Span& a, const Span& b) {
+        return a.p && b.p && a.n && b.n && overlaps(a.p, a.n, b.p, b.n);
+    };
+    for (int o = 0; o < no; ++o) {
+        for (int i = 0; i < ni; ++i) {
+            bool ok = false;
+            for (int k = 0; k < ns; ++k)
+                ok = ok || (same[k][0] == o && same[k][1] == i && out[o].p == in[i].p && out[o].n == in[i].n);
+            if (!ok && hit(out[o], in[i])) return true;
+        }
+        for (int i = o + 1; i < no; ++i)
+            if (hit(out[o], out[i])) return true;
+    }
+    const Span w = {ws, need};
+    for (int i = 0; i < ni; ++i)
+        if (hit(w, in[i])) return true;
+    for (int o = 0; o < no; ++o)
+        if (hit(w, out[o])) return true;
+    return false;
+}
+
+// The caller's workspace, or one allocated on the stream.
+mhla_status take_workspace(void** ws, size_t ws_bytes, size_t need, hipStream_t stream, bool* owned) {
+    *owned = false;
+    if (*ws) {
+        if (ws_bytes < need) return MHLA_ERR_INVALID_ARG;
+        if (need && !aligned16(*ws)) return MHLA_ERR_MISALIGNED;
+        return MHLA_OK;
+    }
+    if (ws_bytes != 0) return MHLA_ERR_INVALID_ARG;
+    if (need == 0) return MHLA_OK;
+    const mhla_status st = alloc_workspace(ws, need, stream);
+    *owned = st == MHLA_OK;
+    return st;
+}
+
+mhla::GatedProblem gated_problem(const Seq& s, const mhla_seq* seq, const GatedPlan& pl, const void* q, const void* k,
+                                 const void* v, const float* g, const int32_t* lens, const float* state,
+                                 hipStream_t stream) {
+    mhla::GatedProblem p;
+    p.B = (int)s.B; p.T = (int)s.T; p.H = (int)s.H; p.HK = (int)s.HK; p.D = (int)s.D;
+    p.bf16 = seq->dtype == MHLA_BF16;
+    p.scale = seq->scale;
+    p.q = q; p.k = k; p.v = v;
+    p.qs = s.qs; p.ks = s.ks; p.vs = s.vs;
+    p.g = g; p.lens = lens; p.s0 = state;
+    p.nseg = pl.nseg; p.seg_chunks = pl.seg_chunks;
+    p.stream = stream;
+    return p;
+}
+
+mhla_status gated_forward_impl(const void* q, const void* k, const void* v, const float* g, const int32_t* lens,
+                               const float* state, const mhla_seq* seq, void* out, float* state_out, void* ws,
+                               size_t ws_bytes, hipStream_t stream) {
+    Seq s;
+    const mhla_status st = check_gated(seq, &s);
+    if (st != MHLA_OK) return st;
+    if (s.empty()) return MHLA_OK;
+    if (s.T > 0 && (!q || !k || !v || !g || !out)) return MHLA_ERR_INVALID_ARG;
+    const void* wide[] = {q, k, v, state, out, state_out};
+    for (const void* x : wide)
+        if (!aligned16(x)) return MHLA_ERR_MISALIGNED;
+    if (!aligned4(g) || !aligned4(lens)) return MHLA_ERR_MISALIGNED;
+    const GatedPlan pl = gated_plan(s, false);
+    const Span in[] = {{q, s.span(s.H, s.qs)}, {k, s.span(s.HK, s.ks)}, {v, s.span(s.HK, s.vs)},
+                       {g, (size_t)(s.tokens() * s.HK) * 4}, {lens, (size_t)s.B * 4}, {state, s.states()}};
+    const Span outs[] = {{out, s.rows(s.H)}, {state_out, s.states()}};
+    const int same[][2] = {{1, 5}};
+    if (spans_clash(in, 6, outs, 2, ws, pl.total, same, 1)) return MHLA_ERR_INVALID_ARG;
+    bool owned;
+    const mhla_status as = take_workspace(&ws, ws_bytes, pl.total, stream, &owned);
+    if (as != MHLA_OK) return as;
+    mhla::GatedForward f;
+    f.p = gated_problem(s, seq, pl, q, k, v, g, lens, state, stream);
+    f.out = out;
+    f.s1 = state_out;
+    f.fst = pl.total ? reinterpret_cast<float*>(static_cast<char*>(ws) + pl.fst) : nullptr;
+    f.fdec = pl.total ? reinterpret_cast<float*>(static_cast<char*>(ws) + pl.dec) : nullptr;
+    const hipError_t err = mhla::run_gated_forward(f);
+    if (owned) (void)hipFreeAsync(ws, stream);
+    return err == hipSuccess ? MHLA_OK : MHLA_ERR_HIP;
+}
+
+mhla_status gated_backward_impl(const void* q, const void* k, const void* v, const float* g, const int32_t* lens,
+                                const float* state, const void* dout, const float* dstate_out, const mhla_seq* seq,
+                                void* dq, void* dk, void* dv, float* dg, float* dstate, void* ws, size_t ws_bytes,
+                                hipStream_t stream) {
+    Seq s;
+    const mhla_status st = check_gated(seq, &s);
+    if (st != MHLA_OK) return st;
+    if (s.empty()) return MHLA_OK;
+    if (s.T > 0 && (!q || !k || !v || !g || !dout || !dq || !dk || !dv || !dg)) return MHLA_ERR_INVALID_ARG;
+    const void* wide[] = {q, k, v, state, dout, dstate_out, dq, dk, dv, dstate};
+    for (const void* x : wide)
+        if (!aligned16(x)) return MHLA_ERR_MISALIGNED;
+    if (!aligned4(g) || !aligned4(lens) || !aligned4(dg)) return MHLA_ERR_MISALIGNED;
+    const GatedPlan pl = gated_plan(s, true);
+    const size_t gates = (size_t)(s.tokens() * s.HK) * 4;
+    const Span in[] = {{q, s.span(s.H, s.qs)}, {k, s.span(s.HK, s.ks)}, {v, s.span(s.HK, s.vs)}, {g, gates},
+                       {lens, (size_t)s.B * 4}, {state, s.states()}, {dout, s.rows(s.H)}, {dstate_out, s.states()}};
+    const Span outs[] = {{dq, s.rows(s.H)}, {dk, s.rows(s.HK)}, {dv, s.rows(s.HK)}, {dg, gates}, {dstate, s.states()}};
+    const int same[][2] = {{4, 7}};
+    if (spans_clash(in, 8, outs, 5, ws, pl.total, same, 1)) return MHLA_ERR_INVALID_ARG;
+    bool owned;
+    const mhla_status as = take_workspace(&ws, ws_bytes, pl.total, stream, &owned);
+    if (as != MHLA_OK) return as;
+    char* base = static_cast<char*>(ws);
+    mhla::GatedBackward f;
+    f.p = gated_problem(s, seq, pl, q, k, v, g, lens, state, stream);
+    f.dout = dout;
+    f.ds1 = dstate_out;
+    f.dq = dq; f.dk = dk; f.dv = dv; f.dg = dg; f.ds0 = dstate;
+    f.fst = reinterpret_cast<float*>(base + pl.fst);
+    f.fdec = reinterpret_cast<float*>(base + pl.dec);
+    f.rst = reinterpret_cast<float*>(base + pl.rst);
+    f.rq = reinterpret_cast<float*>(base + pl.rq);
+    f.rk = reinterpret_cast<float*>(base + pl.rk);
+    const hipError_t err = mhla::run_gated_backward(f);
+    if (owned) (void)hipFreeAsync(ws, stream);
+    return err == hipSuccess ? MHLA_OK : MHLA_ERR_HIP;
+}
+
+mhla_status gated_step_impl(const void* q, const void* k, const void* v, const float* g, const int32_t* slots,
+                            const mhla_seq* seq, float* state, int32_t num_slots, void* out, hipStream_t stream) {
+    Seq s;
+    const mhla_status st = check_gated(seq, &s);
+    if (st != MHLA_OK) return st;
+    if (s.T != 1 || num_slots < 0 || (!slots && num_slots < s.B)) return MHLA_ERR_INVALID_ARG;
+    if (s.empty()) return MHLA_OK;
+    if (!q || !k || !v || !g || !out || (!state && num_slots > 0)) return MHLA_ERR_INVALID_ARG;
+    const void* wide[] = {q, k, v, state, out};
+    for (const void* x : wide)
+        if (!aligned16(x)) return MHLA_ERR_MISALIGNED;
+    if (!aligned4(g) || !aligned4(slots)) return MHLA_ERR_MISALIGNED;
+    const Span in[] = {{q, s.span(s.H, s.qs)}, {k, s.span(s.HK, s.ks)}, {v, s.span(s.HK, s.vs)},
+                       {g, (size_t)(s.B * s.HK) * 4}, {slots, (size_t)s.B * 4}};
+    const Span outs[] = {{out, s.rows(s.H)}, {state, (size_t)(num_slots * s.HK * s.D * s.D) * 4}};
+    if (spans_clash(in, 5, outs, 2, nullptr, 0, nullptr, 0)) return MHLA_ERR_INVALID_ARG;
+    mhla::GatedStep w;
+    w.B = (int)s.B; w.H = (int)s.H; w.HK = (int)s.HK; w.D = (int)s.D;
+    w.bf16 = seq->dtype == MHLA_BF16;
+    w.scale = seq->scale;
+    w.q = q; w.k = k; w.v = v;
+    w.qs = s.qs; w.ks = s.ks; w.vs = s.vs;
+    w.g = g; w.slots = slots; w.state = state; w.nslots = num_slots; w.out = out;
+    w.stream = stream;
+    return mhla::run_gated_step(w) == hipSuccess ? MHLA_OK : MHLA_ERR_HIP;
+}
+
+mhla_status check_rope(const mhla_seq* seq, const mhla_rope* rope, Seq* s, int* pairs) {
+    const mhla_status st = check_seq(seq, s, false);
+    if (st != MHLA_OK) return st;
+    if (s->tokens() >= ((int64_t)1 << 31)) return MHLA_ERR_UNSUPPORTED;   // workgroups of a launch
+    if (!rope) return MHLA_OK;
+    if (rope->style != MHLA_ROPE_HALVES && rope->style != MHLA_ROPE_INTERLEAVED) return MHLA_ERR_INVALID_ARG;
+    if (rope->axes < 1 || rope->axes > 3) return MHLA_ERR_INVALID_ARG;
+    if (!std::isfinite(rope->eps) || rope->eps <= 0.f) return MHLA_ERR_INVALID_ARG;
+    int64_t n = 0;
+    for (int a = 0; a < 3; ++a) {
+        if (rope->section[a] < 0 || (a >= rope->axes && rope->section[a] != 0)) return MHLA_ERR_INVALID_ARG;
+        n += rope->section[a];
+    }
+    if (n <= 0 || n % 8 != 0 || 2 * n > s->D) return MHLA_ERR_INVALID_ARG;
+    *pairs = (int)n;
+    return MHLA_OK;
+}
+
+size_t rope_backward_bytes(const Seq& s) {
+    return (size_t)mhla::qk_rope_groups(s.tokens()) * (size_t)(2 * s.D) * 4;
+}
+
+mhla_status rope_impl(const void* q, const void* k, const float* w_q, const float* w_k, const int32_t* positions,
+                      const float* freq, const mhla_rope* rope, const mhla_seq* seq, void* q_out, void* k_out,
+                      hipStream_t stream, bool backward, const void* dq_out, const void* dk_out, float* dw_q,
+                      float* dw_k, void* ws, size_t ws_bytes) {
+    Seq s;
+    int pairs = 0;
+    const mhla_status st = check_rope(seq, rope, &s, &pairs);
+    if (st != MHLA_OK) return st;
+    if (!rope) return MHLA_ERR_INVALID_ARG;
+    if (!aligned16(dw_q) || !aligned16(dw_k)) return MHLA_ERR_MISALIGNED;
+    if (s.B == 0 || s.T == 0 || (s.H == 0 && s.HK == 0)) {
+        for (float* d : {dw_q, dw_k})
+            if (d && mhla::zero_f32(d, (int)s.D, stream) != hipSuccess) return MHLA_ERR_HIP;
+        return MHLA_OK;
+    }
+    // one side without heads has no tensors
+    if ((s.H && (!q || !q_out)) || (s.HK && (!k || !k_out)) || !positions || !freq) return MHLA_ERR_INVALID_ARG;
+    if (backward && ((s.H && !dq_out) || (s.HK && !dk_out))) return MHLA_ERR_INVALID_ARG;
+    const void* wide[] = {q, k, w_q, w_k, q_out, k_out, dq_out, dk_out};
+    for (const void* x : wide)
+        if (!aligned16(x)) return MHLA_ERR_MISALIGNED;
+    if (!aligned4(positions) || !aligned4(freq)) return MHLA_ERR_MISALIGNED;
+    const size_t wb = (size_t)s.D * 4, need = backward ? rope_backward_bytes(s) : 0;
+    const Span in[] = {{q, s.span(s.H, s.qs)}, {k, s.span(s.HK, s.ks)}, {w_q, wb}, {w_k, wb},
+                       {positions, (size_t)(s.tokens() * rope->axes) * 4}, {freq, (size_t)pairs * 4},
+                       {dq_out, s.rows(s.H)}, {dk_out, s.rows(s.HK)}};
+    const Span outs[] = {{q_out, s.rows(s.H)}, {k_out, s.rows(s.HK)}, {dw_q, wb}, {dw_k, wb}};
+    // spans of equal size: a strided q or k is longer than the output it would share memory with
+    const int fwd[][2] = {{0, 0}, {1, 1}}, bwd[][2] = {{0, 6}, {1, 7}};
+    if (spans_clash(in, 8, outs, 4, ws, need, backward ? bwd : fwd, 2)) return MHLA_ERR_INVALID_ARG;
+    bool owned = false;
+    if (backward) {
+        const mhla_status as = take_workspace(&ws, ws_bytes, need, stream, &owned);
+        if (as != MHLA_OK) return as;
+    }
+    mhla::QkRope r;
+    r.B = (int)s.B; r.T = (int)s.T; r.H = (int)s.H; r.HK = (int)s.HK; r.D = (int)s.D;
+    r.bf16 = seq->dtype == MHLA_BF16;
+    r.style = rope->style; r.axes = rope->axes;
+    for (int a = 0; a < 3; ++a) r.sec[a] = rope->section[a];
+    r.rot = 2 * pairs;
+    r.eps = rope->eps;
+    r.q = q; r.k = k; r.qs = s.qs; r.ks = s.ks;
+    r.wq = w_q; r.wk = w_k; r.pos = positions; r.freq = freq;
+    r.qo = q_out; r.ko = k_out; r.dqo = dq_out; r.dko = dk_out; r.dwq = dw_q; r.dwk = dw_k;
+    r.part = static_cast<float*>(ws);
+    r.groups = mhla::qk_rope_groups(s.tokens());
+    r.stream = stream;
+    const hipError_t err = mhla::run_qk_rope(r, backward);
+    if (owned) (void)hipFreeAsync(ws, stream);
+    return err == hipSuccess ? MHLA_OK : MHLA_ERR_HIP;
+}
+
+}  // namespace
+
+extern "C" {
+
+mhla_status mhla_check_seq(const mhla_seq* seq) {
+    Seq s;
+    return check_gated(seq, &s);
+}
+
+size_t mhla_gated_workspace_bytes(const mhla_seq* seq) {
+    Seq s;
+    return check_gated(seq, &s) != MHLA_OK || s.empty() ? 0 : gated_plan(s, false).total;
+}
+
+size_t mhla_gated_backward_workspace_bytes(const mhla_seq* seq) {
+    Seq s;
+    return check_gated(seq, &s) != MHLA_OK || s.empty() ? 0 : gated_plan(s, true).total;
+}
+
+mhla_status mhla_gated_forward(const void* q, const void* k, const void* v, const float* g, const int32_t* lens,
+                               const float* state, const mhla_seq* seq, void* out, float* state_out, void* ws,
+                               size_t ws_bytes, hipStream_t stream) {
+    return gated_forward_impl(q, k, v, g, lens, state, seq, out, state_out, ws, ws_bytes, stream);
+}
+
+mhla_status mhla_gated_backward(const void* q, const void* k, const void* v, const float* g, const int32_t* lens,
+                                const float* state, const void* dout, const float* dstate_out, const mhla_seq* seq,
+                                void* dq, void* dk, void* dv, float* dg, float* dstate, void* ws, size_t ws_bytes,
+                                hipStream_t stream) {
+    return gated_backward_impl(q, k, v, g, lens, state, dout, dstate_out, seq, dq, dk, dv, dg, dstate, ws, ws_bytes,
+                               stream);
+}
+
+mhla_status mhla_gated_step(const void* q, const void* k, const void* v, const float* g, const int32_t* slots,
+                            const mhla_seq* seq, float* state, int32_t num_slots, void* out, hipStream_t stream) {
+    return gated_step_impl(q, k, v, g, slots, seq, state, num_slots, out, stream);
+}
+
+mhla_status mhla_qk_norm_rope(const void* q, const void* k, const float* w_q, const float* w_k,
+                              const int32_t* positions, const float* freq, const mhla_rope* rope,
+                              const mhla_seq* seq, void* q_out, void* k_out, hipStream_t stream) {
+    return rope_impl(q, k, w_q, w_k, positions, freq, rope, seq, q_out, k_out, stream, false, nullptr, nullptr,
+                     nullptr, nullptr, nullptr, 0);
+}
+
+size_t mhla_qk_norm_rope_backward_workspace_bytes(const mhla_seq* seq) {
+    Seq s;
+    int pairs;
+    if (check_rope(seq, nullptr, &s, &pairs) != MHLA_OK || s.B == 0 || s.T == 0 || (s.H == 0 && s.HK == 0)) return 0;
+    return rope_backward_bytes(s);
+}
+
+mhla_status mhla_qk_norm_rope_backward(const void* q, const void* k, const float* w_q, const float* w_k,
+                                       const int32_t* positions, const float* freq, const mhla_rope* rope,
+                                       const void* dq_out, const void* dk_out, const mhla_seq* seq, void* dq,
+                                       void* dk, float* dw_q, float* dw_k, void* ws, size_t ws_bytes,
+                                       hipStream_t stream) {
+    return rope_impl(q, k, w_q, w_k, positions, freq, rope, seq, dq, dk, stream, true, dq_out, dk_out, dw_q, dw_k, ws,
+                     ws_bytes);
+}
+
+}  // extern "C"
+
+namespace {
 
 // ---------------------------------------------------------------- no-alloc entry point
 //
