@@ -505,8 +505,8 @@ typedef struct mhla_seq {
     int32_t head_dim;    /* d: 32, 64 or 128 */
     int32_t dtype;       /* mhla_dtype of q, k, v, out and their gradients */
     int64_t q_stride;    /* values between a token's q and the next token's; 0: H * d.  At least */
-    int64_t k_stride;    /*   the heads' own values, and a multiple of 16 bytes.  A batch item is */
-    int64_t v_stride;    /*   T tokens: item b starts at token b * T. */
+    int64_t k_stride;    /*   the heads' own values, at most 2^23, and a multiple of 16 bytes.  A batch */
+    int64_t v_stride;    /*   item is T tokens: item b starts at token b * T. */
     float scale;         /* finite */
 } mhla_seq;
 

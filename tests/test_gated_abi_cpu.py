@@ -29,7 +29,7 @@ def seq(**kw):
     ({"kv_heads": 3}, INV), ({"heads": 2, "kv_heads": 4}, INV), ({"scale": math.nan}, INV), ({"scale": math.inf}, INV),
     ({"head_dim": 48}, UNS), ({"head_dim": 256}, UNS), ({"dtype": 2}, UNS), ({"tokens": (1 << 30) + 1}, UNS),
     ({"heads": 65538}, UNS), ({"q_stride": 255}, INV), ({"q_stride": 257}, MIS), ({"q_stride": 256}, mh.MHLA_OK),
-    ({"k_stride": 120}, INV), ({"v_stride": 132}, MIS), ({"v_stride": 1 << 41}, UNS), ({"k_stride": -128}, INV),
+    ({"k_stride": 120}, INV), ({"v_stride": 132}, MIS), ({"v_stride": (1 << 23) + 8}, UNS), ({"k_stride": -128}, INV),
     ({"batch": 1 << 30, "heads": 2, "kv_heads": 2, "tokens": 1}, UNS),
     ({"batch": 4, "tokens": 1 << 30, "heads": 64, "kv_heads": 64}, UNS),
 ])
@@ -100,9 +100,9 @@ def test_workspace_holds_segment_states():
     up = lambda x: (x + 255) // 256 * 256  # noqa: E731
     many = mh.make_seq(64, 4096, 16, 16, 64, mh.MHLA_BF16)
     assert mh.mhla_gated_workspace_bytes(many) == 0              # enough heads: a sequence is one segment
-    few = mh.make_seq(1, 64 * 8, 1, 1, 64, mh.MHLA_BF16)         # two segments of four chunks
-    assert mh.mhla_gated_workspace_bytes(few) == up(3 * 64 * 64 * 4) + up(2 * 4)
-    n = up(3 * 64 * 64 * 4) + up(2 * 4) + up(2 * 64 * 64 * 4) + 2 * up(512 * 4)
+    few = mh.make_seq(1, 64 * 8, 1, 1, 64, mh.MHLA_BF16)         # a segment a chunk
+    assert mh.mhla_gated_workspace_bytes(few) == up(9 * 64 * 64 * 4) + up(8 * 4)
+    n = up(9 * 64 * 64 * 4) + up(8 * 4) + up(8 * 64 * 64 * 4) + 2 * up(512 * 4)
     assert mh.mhla_gated_backward_workspace_bytes(few) == n
 
 

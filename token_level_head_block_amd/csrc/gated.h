@@ -60,6 +60,15 @@ hipError_t run_gated_backward(const GatedBackward& f);
 inline int gated_value_block(int D) { return D < 64 ? D : 64; }
 inline int gated_value_blocks(int D) { return D / gated_value_block(D); }
 
+// Walks (workgroups) that a compute unit holds side by side, by their registers and LDS:
+// bf16 forwards 150 registers and 34 KB at head_dim 64 (three), 212 and 59 KB at 128 (two);
+// backwards 234 and 43 KB (two).  fp32 operands take twice the room.
+inline int gated_walks_per_cu(bool bf16, int D, bool backward) {
+    if (D == 128) return bf16 ? 2 : 1;
+    if (backward) return bf16 || D == 32 ? 2 : 1;
+    return bf16 || D == 32 ? 3 : 2;
+}
+
 struct GatedStep {
     int B, H, HK, D;
     bool bf16;

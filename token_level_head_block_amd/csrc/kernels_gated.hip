@@ -53,6 +53,14 @@ __device__ __forceinline__ f32x4 mma(const Frag<float>& a, const Frag<float>& b,
     return c;
 }
 
+// A packed pair that the compiler takes as a word: it would otherwise round the first value
+// once more by itself to widen it.
+__device__ __forceinline__ uint32_t pack_opaque(float a, float b) {
+    uint32_t w = pack_bf16(a, b);
+    asm("" : "+v"(w));
+    return w;
+}
+
 // Eight fp32 values as the sum of N operands.  bf16: each rounded to nearest, the
 // remainder to the next (the subtractions are exact): one keeps 8 significant bits,
 // two 17, three all 24.
@@ -65,7 +73,7 @@ __device__ __forceinline__ void split(const float (&x)[8], Frag<uint16_t> (&f)[N
     for (int n = 0; n < N; ++n) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const uint32_t w = pack_bf16(r[2 * j], r[2 * j + 1]);
+            const uint32_t w = pack_opaque(r[2 * j], r[2 * j + 1]);
             f[n].v[j] = w;
             if (n + 1 < N) {
                 r[2 * j] -= bf_lo(w);
@@ -128,6 +136,21 @@ struct Tile {
         }
         return f;
     }
+    // the same in token order
+    __device__ static __forceinline__ Frag<E> rows_t(const char* t, int row0, int kk, int lane) {
+        const int row = row0 + (lane & 15), g = lane >> 4;
+        Frag<E> f;
+        if constexpr (sizeof(E) == 2) {
+            const int half = (g & 1) * 8;
+            const u32x2 a = *reinterpret_cast<const u32x2*>(t + at(row, 4 * kk + (g >> 1)) + half);
+            const u32x2 b = *reinterpret_cast<const u32x2*>(t + at(row, 4 * kk + 2 + (g >> 1)) + half);
+            f.v = u32x4{a[0], a[1], b[0], b[1]};
+        } else {
+            f.a = *reinterpret_cast<const f32x4*>(t + at(row, 8 * kk + g));
+            f.b = *reinterpret_cast<const f32x4*>(t + at(row, 8 * kk + 4 + g));
+        }
+        return f;
+    }
     // columns 16 n .. 16 n + 15, contraction over rows 32 kk .. 32 kk + 31, token order
     __device__ static __forceinline__ Frag<E> cols(const char* t, int kk, int n, int lane) {
         const int i = lane & 15, g = lane >> 4;
@@ -163,7 +186,7 @@ __device__ __forceinline__ void put4(char* t, int tile_bytes, int row, int c, co
         char* p = t + Tile<E, W>::at(row, c >> 3) + (c & 4) * 2;
 #pragma unroll
         for (int n = 0; n < N; ++n) {
-            const u32x2 w = {pack_bf16(r[0], r[1]), pack_bf16(r[2], r[3])};
+            const u32x2 w = {pack_opaque(r[0], r[1]), pack_opaque(r[2], r[3])};
             *reinterpret_cast<u32x2*>(p + n * tile_bytes) = w;
             if (n + 1 < N) {
                 r[0] -= bf_lo(w[0]);
@@ -178,42 +201,74 @@ __device__ __forceinline__ void put4(char* t, int tile_bytes, int row, int c, co
 }
 
 // ---------------------------------------------------------------- global memory
-// 16-byte pieces of a chunk's rows (W values from column 0 of `base`) held in registers
-// between their load and their store to LDS; rows from `live` on are zero, whatever the
-// memory holds there.
+// Rows of a chunk go through buffer descriptors over exactly its live rows: a load past
+// them gives zero, whatever the memory holds there, and a store past them is dropped, with
+// no branch and no 64-bit address arithmetic in a lane.  32-bit byte offsets: 64 rows of at
+// most 2^23 values each (checked by the host).
+constexpr int RSRC_FLAGS = 0x00027000;   // raw buffer of dwords
+
+template <typename E>
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_of(const void* p, int64_t tok, int64_t stride, int col, int rows,
+                                                          int width) {
+    const E* base = static_cast<const E*>(p) + tok * stride + col;
+    const int bytes = rows > 0 ? ((rows - 1) * (int)stride + width) * (int)sizeof(E) : 0;
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<E*>(base), 0, bytes, RSRC_FLAGS);
+}
+__device__ __forceinline__ u32x4 load16(__amdgpu_buffer_rsrc_t r, int off) {
+    return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
+}
+__device__ __forceinline__ u32x2 load8b(__amdgpu_buffer_rsrc_t r, int off) {
+    return __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, 0));
+}
+
+// 16-byte pieces of a chunk's rows (W values) held in registers between their load and
+// their store to LDS.
 template <typename E, int W>
 struct Staged {
-    static constexpr int PIECES = GC * Tile<E, W>::NP / THREADS;
+    using TL = Tile<E, W>;
+    static constexpr int PIECES = GC * TL::NP / THREADS, STEP = THREADS / TL::NP;   // rows between a thread's pieces
+    static constexpr bool SAME = STEP % (TL::RP * (TL::NP < 16 ? TL::NP : 16)) == 0;   // and their XOR
     u32x4 r[PIECES];
 
-    __device__ __forceinline__ void load(const E* base, int64_t stride, int live, int tid) {
+    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t rs, int stride, int tid) {
+        const int off = (tid / TL::NP) * stride * (int)sizeof(E) + (tid % TL::NP) * 16;
 #pragma unroll
-        for (int n = 0; n < PIECES; ++n) {
-            const int p = tid + n * THREADS, row = p / Tile<E, W>::NP, pc = p % Tile<E, W>::NP;
-            r[n] = u32x4{0, 0, 0, 0};
-            if (row < live) r[n] = *reinterpret_cast<const u32x4*>(base + (int64_t)row * stride + pc * (16 / (int)sizeof(E)));
-        }
+        for (int n = 0; n < PIECES; ++n) r[n] = load16(rs, off + n * (STEP * stride * (int)sizeof(E)));
     }
     __device__ __forceinline__ void store(char* t, int tid) const {
+        const int row0 = tid / TL::NP, pc = tid % TL::NP;
+        const int a0 = TL::at(row0, pc);
 #pragma unroll
         for (int n = 0; n < PIECES; ++n) {
-            const int p = tid + n * THREADS;
-            *reinterpret_cast<u32x4*>(t + Tile<E, W>::at(p / Tile<E, W>::NP, p % Tile<E, W>::NP)) = r[n];
+            const int a = SAME ? a0 + n * STEP * TL::ROWB : TL::at(row0 + n * STEP, pc);
+            *reinterpret_cast<u32x4*>(t + a) = r[n];
         }
     }
 };
 
-__device__ __forceinline__ void load_row(const uint16_t* p, bool live, Frag<uint16_t>& f) {
-    f.v = u32x4{0, 0, 0, 0};
-    if (live) f.v = *reinterpret_cast<const u32x4*>(p);
+// One row's operand: row order (off at value 8 g) or token order (off at value 4 g).
+__device__ __forceinline__ void load_row(__amdgpu_buffer_rsrc_t r, int off, Frag<uint16_t>& f) { f.v = load16(r, off); }
+__device__ __forceinline__ void load_row(__amdgpu_buffer_rsrc_t r, int off, Frag<float>& f) {
+    f.a = __builtin_bit_cast(f32x4, load16(r, off));
+    f.b = __builtin_bit_cast(f32x4, load16(r, off + 16));
 }
-__device__ __forceinline__ void load_row(const float* p, bool live, Frag<float>& f) {
-    f.a = f.b = f32x4{0.f, 0.f, 0.f, 0.f};
-    if (live) {
-        f.a = *reinterpret_cast<const f32x4*>(p);
-        f.b = *reinterpret_cast<const f32x4*>(p + 4);
-    }
+__device__ __forceinline__ void load_row_t(__amdgpu_buffer_rsrc_t r, int off, Frag<uint16_t>& f) {
+    const u32x2 a = load8b(r, off), b = load8b(r, off + 32);
+    f.v = u32x4{a[0], a[1], b[0], b[1]};
 }
+__device__ __forceinline__ void load_row_t(__amdgpu_buffer_rsrc_t r, int off, Frag<float>& f) {
+    f.a = __builtin_bit_cast(f32x4, load16(r, off));
+    f.b = __builtin_bit_cast(f32x4, load16(r, off + 64));
+}
+// Four neighbouring values of a row.
+__device__ __forceinline__ void store_row4(__amdgpu_buffer_rsrc_t r, int off, const f32x4& x, uint16_t) {
+    const u32x2 w = {pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3])};
+    __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, w), r, off, 0, 0);
+}
+__device__ __forceinline__ void store_row4(__amdgpu_buffer_rsrc_t r, int off, const f32x4& x, float) {
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, x), r, off, 0, 0);
+}
+
 __device__ __forceinline__ f32x4 load4(const uint16_t* p) {
     const u32x2 w = *reinterpret_cast<const u32x2*>(p);
     return f32x4{bf_lo(w[0]), bf_hi(w[0]), bf_lo(w[1]), bf_hi(w[1])};
@@ -232,7 +287,19 @@ __device__ __forceinline__ void store4(float* p, const f32x4& x) { *reinterpret_
 struct Gates {
     float h, f;
 };
-__device__ __forceinline__ Gates gate_sums(float g, int lane) {
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float lanes_below(float x) {
+    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), CTRL, ROWS, 0xf, false));
+}
+template <int CTRL, int ROWS>
+__device__ __forceinline__ void scan_step(Gates& s) {
+    s.h += lanes_below<CTRL, ROWS>(s.h);
+    s.f += lanes_below<CTRL, ROWS>(s.f);
+    const float r = rintf(s.f);
+    s.h += r;
+    s.f -= r;
+}
+__device__ __forceinline__ Gates gate_sums(float g) {
     Gates s;
     const float x = g * LOG2E;
     if (x < -256.f) {
@@ -242,20 +309,60 @@ __device__ __forceinline__ Gates gate_sums(float g, int lane) {
         s.h = rintf(x);
         s.f = fmaf(g, LOG2E, -s.h) + g * LOG2E_LOW;
     }
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-        const float h = __shfl_up(s.h, o, 64), f = __shfl_up(s.f, o, 64);
-        if (lane >= o) {
-            s.h += h;
-            s.f += f;
-            const float r = rintf(s.f);
-            s.h += r;
-            s.f -= r;
-        }
-    }
+    scan_step<0x111, 0xf>(s);   // lanes 1, 2, 4, 8 below in a row of 16 (0 past its start),
+    scan_step<0x112, 0xf>(s);
+    scan_step<0x114, 0xf>(s);
+    scan_step<0x118, 0xf>(s);
+    scan_step<0x142, 0xa>(s);   // then the last lane of rows 0 and 2 into rows 1 and 3,
+    scan_step<0x143, 0xc>(s);   // and lane 31 into rows 2 and 3
     return s;
 }
+__device__ __forceinline__ float lane_value(float x, int lane) {
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x), lane));
+}
 __device__ __forceinline__ float pow2(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// Gate sums and weights of a chunk in LDS, a row of 64 each (row 2 is spare):
+// h, f; kw, weights of the keys in the state; rw, weights of the state in the rows; cw, of
+// a token within its group of 16: 2^(G_b - G_s), G_b the sum at the group's end (backwards
+// 2^(G_s - G_b), G_b the sum before its start), times the pairs' scale.
+constexpr int GATE_ROWS = 6;
+template <bool REV>
+__device__ __forceinline__ void put_gates(float* gh, const Gates& gs, float eh, float ef, float pair_scale,
+                                          float row_scale, float key_scale, int wave, int lane) {
+    // wave 1: kw, wave 2: rw, wave 3: cw (wave 0 fills the spare row), each a power of two of the gate sum's
+    // distance from 0, the chunk's end, or its group's end (backwards: its group's start)
+    const int at = REV ? ((lane & 48) - 1) & 63 : lane | 15;
+    const float gbh = __shfl(gs.h, at, 64), gbf = __shfl(gs.f, at, 64);
+    const bool from0 = REV ? wave == 1 : wave == 2;
+    const float bh = wave == 3 ? gbh : from0 ? 0.f : eh, bf = wave == 3 ? gbf : from0 ? 0.f : ef;
+    const float d = (bh - gs.h) + (bf - gs.f);
+    const float sc = wave == 3 ? pair_scale : wave == 2 ? row_scale : key_scale;
+    gh[(2 + wave) * GC + lane] = sc * pow2(from0 || (REV && wave == 3) ? -d : d);
+    gh[lane] = gs.h;
+    gh[GC + lane] = gs.f;
+}
+// Weights of the tokens of group st in this lane's row (gate sum th + tf): of another group
+// the product of cw and this factor, 0 for a group that the row does not see.
+template <bool REV>
+__device__ __forceinline__ float group_factor(const float* gh, float th, float tf, int st, int wave) {
+    const int at = 16 * st + (REV ? -1 : 15);
+    const float d = (th - gh[at]) + (tf - gh[GC + at]);
+    return pow2((REV ? st > wave : st < wave) ? (REV ? -d : d) : -INFINITY);
+}
+// Of the row's own group, token s = 4 (lane / 16) + j.
+template <bool REV>
+__device__ __forceinline__ f32x4 own_weights(const float* gh, float th, float tf, float scale, int wave, int lane) {
+    const f32x4 sh = *reinterpret_cast<const f32x4*>(gh + 16 * wave + 4 * (lane >> 4));
+    const f32x4 sf = *reinterpret_cast<const f32x4*>(gh + GC + 16 * wave + 4 * (lane >> 4));
+    f32x4 r;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float d = (th - sh[j]) + (tf - sf[j]);
+        r[j] = scale * pow2(REV ? -d : d);
+    }
+    return r;
+}
 
 // ---------------------------------------------------------------- the state in accumulators
 // Tiles of 16 x 16 of the D x EB state, spread over the four waves: wave w holds the row
@@ -359,14 +466,25 @@ struct Walk {
     float pair_scale, row_scale, key_scale;
 };
 
+// Workgroups go to the eight XCDs in turn; this numbering gives each XCD a run of
+// consecutive numbers, so that the heads and value blocks of the same tokens, which read
+// neighbouring (or the same) lines, share an L2 at the same time.
+__device__ __forceinline__ int xcd_run(int blk, int n) {
+    const int x = blk & 7, q = n >> 3, r = n & 7;
+    return x * q + min(x, r) + (blk >> 3);
+}
+
 // A workgroup of four waves walks the chunks of one segment of one (b, kv head), for EB of
 // the value columns.  Wave w has the chunk's tokens 16 w .. 16 w + 15 as rows; products are
 // formed transposed (Y X^T, then Z^T P^T), so that P leaves the accumulators as the next
 // product's operand and a lane stores four neighbouring values of one token.
 // P and S are taken as two bf16 terms (three for the sums r, which are fp32 results), so
 // that the output is rounded once.
+// Pair weights: inside the wave's own 16 tokens each from its two gate sums; with an earlier
+// (later) group of 16 as 2^(G_t - G_b) 2^(G_b - G_s) over the sum at the group's end (before
+// its start), one exponential a row and one a token instead of one a pair.
 template <typename E, int D, int EB, bool REV, bool DOT>
-__global__ void __launch_bounds__(THREADS) gated_walk(Walk w) {
+__global__ void __launch_bounds__(THREADS, sizeof(E) == 2 || D <= 64 ? 2 : 1) gated_walk(Walk w) {
     using TY = Tile<E, D>;
     using TZ = Tile<E, EB>;
     using ST = StateTiles<D, EB>;
@@ -374,31 +492,33 @@ __global__ void __launch_bounds__(THREADS) gated_walk(Walk w) {
     constexpr int NP = sizeof(E) == 4 ? 1 : 2;             // terms of P
     constexpr int KD = D / 32, KE = EB / 32, ET = EB / 16;
     constexpr int YB = GC * TY::ROWB, ZB = GC * TZ::ROWB, SB = EB * TY::ROWB;
-    __shared__ __attribute__((aligned(16))) char lds[YB + ZB + NS * SB + 3 * GC * 4];
+    __shared__ __attribute__((aligned(16))) char lds[YB + ZB + NS * SB + GATE_ROWS * GC * 4];
     char* yt = lds;
     char* zt = lds + YB;
     char* stt = lds + YB + ZB;   // S transposed, [e][c], NS terms
     float* gh = reinterpret_cast<float*>(lds + YB + ZB + NS * SB);
-    float* gf = gh + GC;
-    float* kw = gf + GC;
+    const float* kw = gh + 3 * GC;
+    const float* rw = kw + GC;
+    const float* cw = rw + GC;
 
-    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, li = lane & 15, lg = lane >> 4;
+    const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, li = lane & 15,
+              lg = lane >> 4;
     constexpr int NB = D / EB;
-    int id = blockIdx.x;
+    int id = xcd_run(blockIdx.x, gridDim.x);
     const int eb = id % NB;
     id /= NB;
-    const int seg = id % w.nseg;
-    id /= w.nseg;
-    const int hk = id % w.HK, b = id / w.HK;
+    const int hk = id % w.HK;
+    id /= w.HK;
+    const int seg = id % w.nseg, b = id / w.nseg;
 
     const int T = w.T;
     int len = T;
     if (w.lens) len = min(max(w.lens[b], 0), T);
     const int c0 = seg * w.seg_chunks, c1 = min(c0 + w.seg_chunks, (T + GC - 1) / GC);
     const int live_end = min(c1, (len + GC - 1) / GC);   // chunks from here on hold no live token
-    const int hx_all = w.HK * w.nx, hy_all = w.HK * w.ny;
+    const int hx_all = w.HK * w.nx;
     const int64_t tok0 = (int64_t)b * T;
-    E* const out = static_cast<E*>(w.out);
+    float* const rout = DOT ? w.r + (int64_t)eb * w.B * T * hx_all : nullptr;
 
     typename ST::Acc S;
     load_state<D, EB>(S, w.start ? w.start + ((int64_t)b * w.HK + hk) * w.start_pair + seg * w.start_seg + eb * EB * w.se : nullptr,
@@ -413,150 +533,428 @@ __global__ void __launch_bounds__(THREADS) gated_walk(Walk w) {
             const int row = (int)(p / (w.nx * PC)), rest = (int)(p % (w.nx * PC));
             const int64_t tk = tok0 + t0 + row;
             const int h = hk * w.nx + rest / PC;
-            store4(out + (tk * hx_all + h) * D + eb * EB + (rest % PC) * 4, zero);
-            if (DOT && rest % PC == 0) w.r[((int64_t)eb * w.B * T + tk) * hx_all + h] = 0.f;
+            store4(static_cast<E*>(w.out) + (tk * hx_all + h) * D + eb * EB + (rest % PC) * 4, zero);
+            if (DOT && rest % PC == 0) rout[tk * hx_all + h] = 0.f;
         }
     }
 
-    const int items = max(live_end - c0, 0) * w.ny;
+    const int chunks = max(live_end - c0, 0);
+    const int first = REV ? live_end - 1 : c0, dir = REV ? -1 : 1;
+    const int nx = REV ? 1 : w.nx, ny = REV ? w.ny : 1;   // backwards it is Y and Z that a group has several of
+    const int tl = 16 * wave + li;                        // this lane's token in a chunk
+    constexpr int ES = (int)sizeof(E);
     Staged<E, D> ys;
     Staged<E, EB> zs;
     float graw = 0.f;
-    auto fetch = [&](int it) {
-        const int ci = it / w.ny, hy = it - ci * w.ny;
-        const int c = REV ? live_end - 1 - ci : c0 + ci;
-        const int live = min(len - c * GC, GC);
+    // a chunk past the walk's end has no rows
+    auto fetch = [&](int ci, int hy) {
+        const int c = first + dir * ci;
+        const int live = ci < chunks ? min(len - c * GC, GC) : 0;
         const int64_t tk = tok0 + (int64_t)c * GC;
-        const int h = hk * w.ny + hy;
-        ys.load(static_cast<const E*>(w.y.p) + tk * w.y.stride + h * D, w.y.stride, live, tid);
-        zs.load(static_cast<const E*>(w.z.p) + tk * w.z.stride + h * D + eb * EB, w.z.stride, live, tid);
-        if (hy == 0) graw = lane < live ? w.g[(tk + lane) * w.HK + hk] : 0.f;
+        const int h = hk * ny + hy;
+        ys.load(rows_of<E>(w.y.p, tk, w.y.stride, h * D, live, D), (int)w.y.stride, tid);
+        zs.load(rows_of<E>(w.z.p, tk, w.z.stride, h * D + eb * EB, live, EB), (int)w.z.stride, tid);
+        graw = __int_as_float(__builtin_amdgcn_raw_buffer_load_b32(rows_of<float>(w.g, tk, w.HK, hk, live, 1), lane * w.HK * 4, 0, 0));
     };
-    if (items > 0) fetch(0);
+    Frag<E> xf[KD], x2f[DOT ? KE : 1];
+    auto fetch_x = [&](int ci, int hx, Frag<E> (&x)[KD], Frag<E> (&x2)[DOT ? KE : 1]) {
+        const int c = first + dir * ci;
+        const int live = ci < chunks ? min(len - c * GC, GC) : 0;
+        const int64_t tk = tok0 + (int64_t)c * GC;
+        const int h = hk * nx + hx;
+        const __amdgpu_buffer_rsrc_t rx = rows_of<E>(w.x.p, tk, w.x.stride, h * D, live, D);
+#pragma unroll
+        for (int kk = 0; kk < KD; ++kk) load_row(rx, (tl * (int)w.x.stride + 8 * lg + 32 * kk) * ES, x[kk]);
+        if constexpr (DOT) {
+            const __amdgpu_buffer_rsrc_t r2 = rows_of<E>(w.x2.p, tk, w.x2.stride, h * D + eb * EB, live, EB);
+#pragma unroll
+            for (int kk = 0; kk < KE; ++kk) load_row_t(r2, (tl * (int)w.x2.stride + 4 * lg + 32 * kk) * ES, x2[kk]);
+        }
+    };
+    fetch(0, 0);
+    fetch_x(0, 0, xf, x2f);
 
     f32x4 o[ET];
     float rsum = 0.f;
-    Gates gs = {0.f, 0.f};
-    float eh = 0.f, ef = 0.f;
-    for (int it = 0; it < items; ++it) {
-        const int ci = it / w.ny, hy = it - ci * w.ny;
-        const int c = REV ? live_end - 1 - ci : c0 + ci;
-        const int t = c * GC + 16 * wave + li;    // this lane's token
-        const bool live = t < len;
-        __syncthreads();                          // the last item's reads are over
-        ys.store(yt, tid);
-        zs.store(zt, tid);
-        if (hy == 0) {
-            gs = gate_sums(graw, lane);
-            eh = __shfl(gs.h, 63, 64);
-            ef = __shfl(gs.f, 63, 64);
-            if (wave == 0) {
-                gh[lane] = gs.h;
-                gf[lane] = gs.f;
-                kw[lane] = w.key_scale * (REV ? pow2(gs.h + gs.f) : pow2((eh - gs.h) + (ef - gs.f)));
+    for (int ci = 0; ci < chunks; ++ci) {
+        const int c = first + dir * ci;
+        const bool live = c * GC + tl < len;
+        const int rows = min(T - c * GC, GC);
+        const int64_t tk0 = tok0 + (int64_t)c * GC;
+        const Gates gs = gate_sums(graw);
+        const float eh = lane_value(gs.h, 63), ef = lane_value(gs.f, 63);
+        float decay = pow2(eh + ef);
+        for (int hy = 0; hy < ny; ++hy) {
+            __syncthreads();                      // the last tile's reads are over
+            ys.store(yt, tid);
+            zs.store(zt, tid);
+            if (!REV || hy == 0) {
+                put_gates<REV>(gh, gs, eh, ef, w.pair_scale, w.row_scale, w.key_scale, wave, lane);
+#pragma unroll
+                for (int a = 0; a < ST::CW; ++a)
+#pragma unroll
+                    for (int e = 0; e < ST::EW; ++e)
+                        put4<E, D, NS>(stt, SB, 16 * ST::et(wave, e) + li, 16 * ST::ct(wave, a) + 4 * lg, S[a][e]);
             }
-#pragma unroll
-            for (int a = 0; a < ST::CW; ++a)
-#pragma unroll
-                for (int e = 0; e < ST::EW; ++e)
-                    put4<E, D, NS>(stt, SB, 16 * ST::et(wave, e) + li, 16 * ST::ct(wave, a) + 4 * lg, S[a][e]);
-        }
-        __syncthreads();
-        if (it + 1 < items) fetch(it + 1);
+            __syncthreads();
+            const bool last_y = hy + 1 == ny;
+            fetch(last_y ? ci + 1 : ci, last_y ? 0 : hy + 1);
 
-        const float th = gh[16 * wave + li], tf = gf[16 * wave + li];
-        for (int hx = 0; hx < w.nx; ++hx) {
-            const int h = hk * w.nx + hx;
-            const int64_t tk = tok0 + t;
-            Frag<E> xf[KD];
+            const float th = gh[tl], tf = gh[GC + tl], trw = rw[tl];
+            for (int hx = 0; hx < nx; ++hx) {
+                const bool last_x = hx + 1 == nx;
+                asm volatile("" ::: "memory");    // reads of the tiles stay in the loop: hoisted, they fill the registers
+                Frag<E> xn[KD], x2n[DOT ? KE : 1];
+                if (!REV || last_y) fetch_x(last_x ? ci + 1 : ci, last_x ? 0 : hx + 1, xn, x2n);
+                if (!REV || hy == 0) {
+                    // from the state: o = S^T x
+                    rsum = 0.f;
 #pragma unroll
-            for (int kk = 0; kk < KD; ++kk)
-                load_row(static_cast<const E*>(w.x.p) + tk * w.x.stride + h * D + 32 * kk + 8 * lg, live, xf[kk]);
-            Frag<E> x2f[DOT ? KE : 1];
-            const E* x2 = DOT ? static_cast<const E*>(w.x2.p) + tk * w.x2.stride + h * D + eb * EB : nullptr;
-            if constexpr (DOT) {
+                    for (int e = 0; e < ET; ++e) {
+                        f32x4 acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int kk = 0; kk < KE; ++kk) load_row(x2 + 32 * kk + 8 * lg, live, x2f[kk]);
-            }
-            if (hy == 0) {
-                // from the state: o = S^T x
-                const float rf = w.row_scale * (REV ? pow2((eh - th) + (ef - tf)) : pow2(th + tf));
-                rsum = 0.f;
+                        for (int n = NS - 1; n >= 0; --n)
 #pragma unroll
-                for (int e = 0; e < ET; ++e) {
-                    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                    for (int n = NS - 1; n >= 0; --n)
-#pragma unroll
-                        for (int kk = 0; kk < KD; ++kk)
-                            acc = mma(TY::rows(stt + n * SB, 16 * e, kk, lane), xf[kk], acc);
-                    o[e] = acc * rf;
-                    if constexpr (DOT) {
-                        f32x4 u = {0.f, 0.f, 0.f, 0.f};
-                        if (live) u = load4(x2 + 16 * e + 4 * lg);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) rsum += u[j] * o[e][j];
+                            for (int kk = 0; kk < KD; ++kk)
+                                acc = mma(TY::rows(stt + n * SB, 16 * e, kk, lane), xf[kk], acc);
+                        o[e] = acc * trw;
                     }
-                }
-            }
-            // from the chunk: 32 tokens s at a time, those that some row of the wave sees
+                    if constexpr (DOT) {
 #pragma unroll
-            for (int kk = 0; kk < GC / 32; ++kk) {
-                if (REV ? 2 * kk + 1 < wave : 2 * kk > wave) continue;
-                float p[8];
+                        for (int kk = 0; kk < KE; ++kk) {
+                            float u[8];
+                            widen(x2f[kk], u);
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const int st = 2 * kk + u;
-                    f32x4 acc = {0.f, 0.f, 0.f, 0.f}, m = {0.f, 0.f, 0.f, 0.f};
-                    if (REV ? st >= wave : st <= wave) {
-#pragma unroll
-                        for (int k = 0; k < KD; ++k) acc = mma(TY::rows(yt, 16 * st, k, lane), xf[k], acc);
-                        if constexpr (DOT) {
-#pragma unroll
-                            for (int k = 0; k < KE; ++k) m = mma(TZ::rows(zt, 16 * st, k, lane), x2f[k], m);
+                            for (int j = 0; j < 4; ++j) rsum += u[j] * o[2 * kk][j] + u[4 + j] * o[2 * kk + 1][j];
                         }
                     }
-                    const f32x4 sh = *reinterpret_cast<const f32x4*>(gh + 16 * st + 4 * lg);
-                    const f32x4 sf = *reinterpret_cast<const f32x4*>(gf + 16 * st + 4 * lg);
+                }
+                // weights of the tokens s of the chunk: groups of 16 that come before (after) the wave's own,
+                // the others' weight being 0, and its own
+                float p[GC / 16][4];
+#pragma unroll
+                for (int st = 0; st < GC / 16; ++st) {
+                    if (st == (REV ? 0 : GC / 16 - 1)) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) p[st][j] = 0.f;
+                        continue;
+                    }
+                    f32x4 acc = {0.f, 0.f, 0.f, 0.f}, m = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int k = 0; k < KD; ++k) acc = mma(TY::rows(yt, 16 * st, k, lane), xf[k], acc);
+                    if constexpr (DOT) {
+#pragma unroll
+                        for (int k = 0; k < KE; ++k) m = mma(TZ::rows_t(zt, 16 * st, k, lane), x2f[k], m);
+                    }
+                    const float rf = group_factor<REV>(gh, th, tf, st, wave);
+                    const f32x4 cs = *reinterpret_cast<const f32x4*>(cw + 16 * st + 4 * lg);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        const int s = 16 * st + 4 * lg + j, tt = 16 * wave + li;
-                        const float d = (th - sh[j]) + (tf - sf[j]);
-                        const float dec = w.pair_scale * pow2(REV ? -d : d);
-                        const bool sees = REV ? s >= tt : s <= tt;
-                        const float v = sees ? acc[j] * dec : 0.f;
-                        p[4 * u + j] = v;
-                        if constexpr (DOT) rsum += sees && s != tt ? v * m[j] : 0.f;
+                        p[st][j] = acc[j] * (cs[j] * rf);
+                        if constexpr (DOT) rsum += p[st][j] * m[j];
                     }
                 }
-                Frag<E> pf[NP];
-                split<NP>(p, pf);
+                {
+                    f32x4 acc = {0.f, 0.f, 0.f, 0.f}, m = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int e = 0; e < ET; ++e) {
-                    const Frag<E> z = TZ::cols(zt, kk, e, lane);
+                    for (int k = 0; k < KD; ++k) acc = mma(TY::rows(yt, 16 * wave, k, lane), xf[k], acc);
+                    if constexpr (DOT) {
 #pragma unroll
-                    for (int n = NP - 1; n >= 0; --n) o[e] = mma(z, pf[n], o[e]);
+                        for (int k = 0; k < KE; ++k) m = mma(TZ::rows_t(zt, 16 * wave, k, lane), x2f[k], m);
+                    }
+                    const f32x4 ow = own_weights<REV>(gh, th, tf, w.pair_scale, wave, lane);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int s = 4 * lg + j;
+                        const float v = acc[j] * ow[j];
+                        const float own = (REV ? s >= li : s <= li) ? v : 0.f;
+                        if constexpr (DOT) rsum += s != li ? own * m[j] : 0.f;
+#pragma unroll
+                        for (int st = 0; st < GC / 16; ++st) p[st][j] = st == wave ? own : p[st][j];
+                    }
                 }
-            }
-            if (hy == w.ny - 1) {
-                if (t < T) {
+#pragma unroll
+                for (int kk = 0; kk < GC / 32; ++kk) {
+                    float q[8];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        q[j] = p[2 * kk][j];
+                        q[4 + j] = p[2 * kk + 1][j];
+                    }
+                    Frag<E> pf[NP];
+                    split<NP>(q, pf);
+#pragma unroll
+                    for (int e = 0; e < ET; ++e) {
+                        const Frag<E> z = TZ::cols(zt, kk, e, lane);
+#pragma unroll
+                        for (int n = NP - 1; n >= 0; --n) o[e] = mma(z, pf[n], o[e]);
+                    }
+                }
+                if (!REV || last_y) {
+                    const int h = hk * nx + hx;
+                    const __amdgpu_buffer_rsrc_t ro = rows_of<E>(w.out, tk0, (int64_t)hx_all * D, h * D + eb * EB, rows, EB);
                     const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                     for (int e = 0; e < ET; ++e)
-                        store4(out + (tk * hx_all + h) * D + eb * EB + 16 * e + 4 * lg, live ? o[e] : zero);
-                }
-                if constexpr (DOT) {
-                    float s = rsum + shfl_xor(rsum, 16);
-                    s += shfl_xor(s, 32);
-                    if (lg == 0 && t < T) w.r[((int64_t)eb * w.B * T + tk) * hx_all + h] = live ? s : 0.f;
+                        store_row4(ro, (tl * hx_all * D + 16 * e + 4 * lg) * ES, live ? o[e] : zero, E());
+                    if constexpr (DOT) {
+                        float s = rsum + shfl_xor(rsum, 16);
+                        s += shfl_xor(s, 32);     // all four lanes of a token store the same sum
+                        const __amdgpu_buffer_rsrc_t rr = rows_of<float>(rout, tk0, hx_all, h, rows, 1);
+                        __builtin_amdgcn_raw_buffer_store_b32(__float_as_int(live ? s : 0.f), rr, tl * hx_all * 4, 0, 0);
+                    }
+#pragma unroll
+                    for (int kk = 0; kk < KD; ++kk) xf[kk] = xn[kk];
+                    if constexpr (DOT) {
+#pragma unroll
+                        for (int kk = 0; kk < KE; ++kk) x2f[kk] = x2n[kk];
+                    }
                 }
             }
+            update_state<E, D, EB>(S, yt, zt, kw, decay, wave, lane);
+            decay = 1.f;
         }
-        update_state<E, D, EB>(S, yt, zt, kw, hy == 0 ? pow2(eh + ef) : 1.f, wave, lane);
     }
     if (w.end && (REV ? seg == 0 : seg == w.nseg - 1))
         store_state<D, EB>(S, w.end + ((int64_t)b * w.HK + hk) * D * D + eb * EB * w.se, w.sc, w.se, wave, lane);
-    (void)hy_all;
+}
+
+// ---------------------------------------------------------------- dk and dv together
+// Backwards over a segment with X = k and v, Y = q, Z = do: the pair products q . k and
+// do . v serve dk, dv and k . dk alike, the tiles are read once and the state's gradient D is
+// summed once, where two walks would do each twice.  D lies in LDS once, transposed ([e][c]):
+// dv contracts it over c (its columns), dk over e (its rows, by transposing reads), so k and
+// v are held in token order.  D <= 64: at 128 the state of all columns leaves room for one
+// workgroup of a compute unit, and dk and dv are walks of their own.
+struct Back {
+    Role q, k, v, dout;
+    void* dk;
+    void* dv;            // [B, T, HK, D]
+    float* r;            // k . dk without a token's own term, [B, T, HK]
+    const float* g;
+    const int32_t* lens;
+    const float* start;  // gradient of the state behind each segment, [B*HK][nseg][D*D]
+    float* end;          // gradient of the initial state, or nullptr
+    int B, T, HK, G, nseg, seg_chunks;
+    float scale;
+};
+
+template <typename E, int D>
+__global__ void __launch_bounds__(THREADS, sizeof(E) == 2 || D == 32 ? 2 : 1) gated_back(Back w) {
+    using TL = Tile<E, D>;
+    using ST = StateTiles<D, D>;
+    constexpr int NS = sizeof(E) == 4 ? 1 : 3;             // terms of D (two for dv, three for k . dk)
+    constexpr int NSV = sizeof(E) == 4 ? 1 : 2;
+    constexpr int NP = sizeof(E) == 4 ? 1 : 2;
+    constexpr int KD = D / 32, DT = D / 16, ES = (int)sizeof(E);
+    constexpr int TB = GC * TL::ROWB, SB = D * TL::ROWB;
+    __shared__ __attribute__((aligned(16))) char lds[2 * TB + NS * SB + GATE_ROWS * GC * 4];
+    char* yt = lds;
+    char* zt = lds + TB;
+    char* stt = lds + 2 * TB;
+    float* gh = reinterpret_cast<float*>(lds + 2 * TB + NS * SB);
+    const float* kw = gh + 3 * GC;
+    const float* rw = kw + GC;
+    const float* cw = rw + GC;
+
+    const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, li = lane & 15,
+              lg = lane >> 4;
+    int id = xcd_run(blockIdx.x, gridDim.x);
+    const int hk = id % w.HK;
+    id /= w.HK;
+    const int seg = id % w.nseg, b = id / w.nseg;
+    const int T = w.T;
+    int len = T;
+    if (w.lens) len = min(max(w.lens[b], 0), T);
+    const int c0 = seg * w.seg_chunks, c1 = min(c0 + w.seg_chunks, (T + GC - 1) / GC);
+    const int live_end = min(c1, (len + GC - 1) / GC);
+    const int64_t tok0 = (int64_t)b * T, pair = (int64_t)b * w.HK + hk;
+
+    typename ST::Acc S;
+    load_state<D, D>(S, w.start + (pair * w.nseg + seg) * D * D, D, 1, wave, lane);
+
+    {   // rows of dead chunks are zero
+        const int t0 = max(c0, live_end) * GC, n = min(c1 * GC, T) - t0;
+        constexpr int PC = D / 4;
+        const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+        for (int p = tid; p < n * PC; p += THREADS) {
+            const int64_t tk = tok0 + t0 + p / PC, at = (tk * w.HK + hk) * D + (p % PC) * 4;
+            store4(static_cast<E*>(w.dk) + at, zero);
+            store4(static_cast<E*>(w.dv) + at, zero);
+            if (p % PC == 0) w.r[tk * w.HK + hk] = 0.f;
+        }
+    }
+
+    const int chunks = max(live_end - c0, 0);
+    const int tl = 16 * wave + li;
+    Staged<E, D> ys, zs;
+    float graw = 0.f;
+    auto fetch = [&](int ci, int hy) {
+        const int c = live_end - 1 - ci;
+        const int live = ci < chunks ? min(len - c * GC, GC) : 0;
+        const int64_t tk = tok0 + (int64_t)c * GC;
+        const int h = hk * w.G + hy;
+        ys.load(rows_of<E>(w.q.p, tk, w.q.stride, h * D, live, D), (int)w.q.stride, tid);
+        zs.load(rows_of<E>(w.dout.p, tk, w.dout.stride, h * D, live, D), (int)w.dout.stride, tid);
+        graw = __int_as_float(__builtin_amdgcn_raw_buffer_load_b32(rows_of<float>(w.g, tk, w.HK, hk, live, 1), lane * w.HK * 4, 0, 0));
+    };
+    Frag<E> kf[KD], vf[KD], kn[KD], vn[KD];
+    auto fetch_x = [&](int ci, Frag<E> (&k)[KD], Frag<E> (&v)[KD]) {
+        const int c = live_end - 1 - ci;
+        const int live = ci < chunks ? min(len - c * GC, GC) : 0;
+        const int64_t tk = tok0 + (int64_t)c * GC;
+        const __amdgpu_buffer_rsrc_t rk = rows_of<E>(w.k.p, tk, w.k.stride, hk * D, live, D);
+        const __amdgpu_buffer_rsrc_t rv = rows_of<E>(w.v.p, tk, w.v.stride, hk * D, live, D);
+#pragma unroll
+        for (int kk = 0; kk < KD; ++kk) {
+            load_row_t(rk, (tl * (int)w.k.stride + 4 * lg + 32 * kk) * ES, k[kk]);
+            load_row_t(rv, (tl * (int)w.v.stride + 4 * lg + 32 * kk) * ES, v[kk]);
+        }
+    };
+    fetch(0, 0);
+    fetch_x(0, kf, vf);
+
+    f32x4 ok[DT], ov[DT];
+    float rsum = 0.f;
+    for (int ci = 0; ci < chunks; ++ci) {
+        const int c = live_end - 1 - ci;
+        const bool live = c * GC + tl < len;
+        const int rows = min(T - c * GC, GC);
+        const int64_t tk0 = tok0 + (int64_t)c * GC;
+        const Gates gs = gate_sums(graw);
+        const float eh = lane_value(gs.h, 63), ef = lane_value(gs.f, 63);
+        float decay = pow2(eh + ef);
+        for (int hy = 0; hy < w.G; ++hy) {
+            __syncthreads();                      // the last tile's reads are over
+            ys.store(yt, tid);
+            zs.store(zt, tid);
+            if (hy == 0) {
+                put_gates<true>(gh, gs, eh, ef, w.scale, 1.f, w.scale, wave, lane);
+#pragma unroll
+                for (int a = 0; a < ST::CW; ++a)
+#pragma unroll
+                    for (int e = 0; e < ST::EW; ++e)
+                        put4<E, D, NS>(stt, SB, 16 * ST::et(wave, e) + li, 16 * ST::ct(wave, a) + 4 * lg, S[a][e]);
+            }
+            __syncthreads();
+            const bool last = hy + 1 == w.G;
+            fetch(last ? ci + 1 : ci, last ? 0 : hy + 1);
+            if (hy == 0) {
+                fetch_x(ci + 1, kn, vn);
+                // from the state: dv = D^T k, dk = D v
+                const float trw = rw[tl];
+                rsum = 0.f;
+#pragma unroll
+                for (int e = 0; e < DT; ++e) {
+                    f32x4 a = {0.f, 0.f, 0.f, 0.f}, c2 = a;
+#pragma unroll
+                    for (int n = NS - 1; n >= 0; --n)
+#pragma unroll
+                        for (int kk = 0; kk < KD; ++kk) {
+                            if (n < NSV) a = mma(TL::rows_t(stt + n * SB, 16 * e, kk, lane), kf[kk], a);
+                            c2 = mma(TL::cols(stt + n * SB, kk, e, lane), vf[kk], c2);
+                        }
+                    ov[e] = a * trw;
+                    ok[e] = c2 * trw;
+                }
+#pragma unroll
+                for (int kk = 0; kk < KD; ++kk) {
+                    float u[8];
+                    widen(kf[kk], u);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) rsum += u[j] * ok[2 * kk][j] + u[4 + j] * ok[2 * kk + 1][j];
+                }
+            }
+            const float th = gh[tl], tf = gh[GC + tl];
+            float p[GC / 16][4], m[GC / 16][4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) p[0][j] = m[0][j] = 0.f;
+#pragma unroll
+            for (int st = 1; st < GC / 16; ++st) {
+                f32x4 a = {0.f, 0.f, 0.f, 0.f}, c2 = a;
+#pragma unroll
+                for (int k = 0; k < KD; ++k) {
+                    a = mma(TL::rows_t(yt, 16 * st, k, lane), kf[k], a);
+                    c2 = mma(TL::rows_t(zt, 16 * st, k, lane), vf[k], c2);
+                }
+                const float rf = group_factor<true>(gh, th, tf, st, wave);
+                const f32x4 cs = *reinterpret_cast<const f32x4*>(cw + 16 * st + 4 * lg);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float wt = cs[j] * rf;
+                    p[st][j] = a[j] * wt;
+                    m[st][j] = c2[j] * wt;
+                    rsum += p[st][j] * c2[j];
+                }
+            }
+            {
+                f32x4 a = {0.f, 0.f, 0.f, 0.f}, c2 = a;
+#pragma unroll
+                for (int k = 0; k < KD; ++k) {
+                    a = mma(TL::rows_t(yt, 16 * wave, k, lane), kf[k], a);
+                    c2 = mma(TL::rows_t(zt, 16 * wave, k, lane), vf[k], c2);
+                }
+                const f32x4 ow = own_weights<true>(gh, th, tf, w.scale, wave, lane);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int t = 4 * lg + j;
+                    const float pv = t >= li ? a[j] * ow[j] : 0.f, mv = t >= li ? c2[j] * ow[j] : 0.f;
+                    rsum += t != li ? pv * c2[j] : 0.f;
+#pragma unroll
+                    for (int st = 0; st < GC / 16; ++st) {
+                        p[st][j] = st == wave ? pv : p[st][j];
+                        m[st][j] = st == wave ? mv : m[st][j];
+                    }
+                }
+            }
+#pragma unroll
+            for (int kk = 0; kk < GC / 32; ++kk) {
+                float pq[8], mq[8];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    pq[j] = p[2 * kk][j];
+                    pq[4 + j] = p[2 * kk + 1][j];
+                    mq[j] = m[2 * kk][j];
+                    mq[4 + j] = m[2 * kk + 1][j];
+                }
+                Frag<E> pf[NP], mf[NP];
+                split<NP>(pq, pf);
+                split<NP>(mq, mf);
+#pragma unroll
+                for (int e = 0; e < DT; ++e) {
+                    const Frag<E> z = TL::cols(zt, kk, e, lane), y = TL::cols(yt, kk, e, lane);
+#pragma unroll
+                    for (int n = NP - 1; n >= 0; --n) {
+                        ov[e] = mma(z, pf[n], ov[e]);
+                        ok[e] = mma(y, mf[n], ok[e]);
+                    }
+                }
+            }
+            if (last) {
+                const __amdgpu_buffer_rsrc_t rv = rows_of<E>(w.dv, tk0, (int64_t)w.HK * D, hk * D, rows, D);
+                const __amdgpu_buffer_rsrc_t rk = rows_of<E>(w.dk, tk0, (int64_t)w.HK * D, hk * D, rows, D);
+                const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int e = 0; e < DT; ++e) {
+                    const int off = (tl * w.HK * D + 16 * e + 4 * lg) * ES;
+                    store_row4(rv, off, live ? ov[e] : zero, E());
+                    store_row4(rk, off, live ? ok[e] : zero, E());
+                }
+                float s = rsum + shfl_xor(rsum, 16);
+                s += shfl_xor(s, 32);             // all four lanes of a token store the same sum
+                __builtin_amdgcn_raw_buffer_store_b32(__float_as_int(live ? s : 0.f), rows_of<float>(w.r, tk0, w.HK, hk, rows, 1),
+                                                      tl * w.HK * 4, 0, 0);
+            }
+            update_state<E, D, D>(S, yt, zt, kw, decay, wave, lane);
+            decay = 1.f;
+        }
+#pragma unroll
+        for (int kk = 0; kk < KD; ++kk) {
+            kf[kk] = kn[kk];
+            vf[kk] = vn[kk];
+        }
+    }
+    if (w.end && seg == 0) store_state<D, D>(S, w.end + pair * D * D, D, 1, wave, lane);
 }
 
 // ---------------------------------------------------------------- segments
@@ -586,16 +984,16 @@ __global__ void __launch_bounds__(THREADS) gated_local(Local w) {
     char* yt = lds;
     char* zt = lds + YB;
     float* kw = reinterpret_cast<float*>(lds + YB + ZB);
-    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+    const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
     constexpr int NB = D / EB;
-    int id = blockIdx.x;
+    int id = xcd_run(blockIdx.x, gridDim.x);
     const int eb = id % NB;
     id /= NB;
+    const int hk = id % w.HK;
+    id /= w.HK;
     const int role = id % w.roles;
     id /= w.roles;
-    const int seg = id % w.nseg;
-    id /= w.nseg;
-    const int hk = id % w.HK, b = id / w.HK;
+    const int seg = id % w.nseg, b = id / w.nseg;
     const int T = w.T;
     int len = T;
     if (w.lens) len = min(max(w.lens[b], 0), T);
@@ -614,38 +1012,38 @@ __global__ void __launch_bounds__(THREADS) gated_local(Local w) {
         for (int e = 0; e < ST::EW; ++e) S[a][e] = zero;
     float dec = 1.f;
 
-    const int items = max(live_end - c0, 0) * ny;
+    const int chunks = max(live_end - c0, 0);
+    const int first = role ? live_end - 1 : c0, dir = role ? -1 : 1;
     Staged<E, D> ys;
     Staged<E, EB> zs;
     float graw = 0.f;
-    auto fetch = [&](int it) {
-        const int ci = it / ny, hy = it - ci * ny;
-        const int c = role ? live_end - 1 - ci : c0 + ci;
-        const int live = min(len - c * GC, GC);
+    auto fetch = [&](int ci, int hy) {
+        const int c = first + dir * ci;
+        const int live = ci < chunks ? min(len - c * GC, GC) : 0;
         const int64_t tk = tok0 + (int64_t)c * GC;
         const int h = hk * ny + hy;
-        ys.load(static_cast<const E*>(ry.p) + tk * ry.stride + h * D, ry.stride, live, tid);
-        zs.load(static_cast<const E*>(rz.p) + tk * rz.stride + h * D + eb * EB, rz.stride, live, tid);
-        if (hy == 0) graw = lane < live ? w.g[(tk + lane) * w.HK + hk] : 0.f;
+        ys.load(rows_of<E>(ry.p, tk, ry.stride, h * D, live, D), (int)ry.stride, tid);
+        zs.load(rows_of<E>(rz.p, tk, rz.stride, h * D + eb * EB, live, EB), (int)rz.stride, tid);
+        graw = __int_as_float(__builtin_amdgcn_raw_buffer_load_b32(rows_of<float>(w.g, tk, w.HK, hk, live, 1), lane * w.HK * 4, 0, 0));
     };
-    if (items > 0) fetch(0);
-    float decay = 1.f;
-    for (int it = 0; it < items; ++it) {
-        const int hy = it % ny;
-        __syncthreads();
-        ys.store(yt, tid);
-        zs.store(zt, tid);
-        decay = 1.f;
-        if (hy == 0) {
-            const Gates gs = gate_sums(graw, lane);
-            const float eh = __shfl(gs.h, 63, 64), ef = __shfl(gs.f, 63, 64);
-            if (wave == 0) kw[lane] = key_scale * (role ? pow2(gs.h + gs.f) : pow2((eh - gs.h) + (ef - gs.f)));
-            decay = pow2(eh + ef);
-            dec *= decay;
+    fetch(0, 0);
+    for (int ci = 0; ci < chunks; ++ci) {
+        const Gates gs = gate_sums(graw);
+        const float eh = lane_value(gs.h, 63), ef = lane_value(gs.f, 63);
+        float decay = pow2(eh + ef);
+        dec *= decay;
+        const float key = key_scale * (role ? pow2(gs.h + gs.f) : pow2((eh - gs.h) + (ef - gs.f)));
+        for (int hy = 0; hy < ny; ++hy) {
+            __syncthreads();
+            ys.store(yt, tid);
+            zs.store(zt, tid);
+            kw[lane] = key;                       // every wave the same
+            __syncthreads();
+            const bool last_y = hy + 1 == ny;
+            fetch(last_y ? ci + 1 : ci, last_y ? 0 : hy + 1);
+            update_state<E, D, EB>(S, yt, zt, kw, decay, wave, lane);
+            decay = 1.f;
         }
-        __syncthreads();
-        if (it + 1 < items) fetch(it + 1);
-        update_state<E, D, EB>(S, yt, zt, kw, decay, wave, lane);
     }
     const int64_t pair = (int64_t)b * w.HK + hk;
     float* st = (role ? w.st[1] : w.st[0]) + pair * (role ? w.pair[1] : w.pair[0]) + (role ? w.first[1] : w.first[0]) +
@@ -655,62 +1053,73 @@ __global__ void __launch_bounds__(THREADS) gated_local(Local w) {
 }
 
 // Joins the segments: fst[j] becomes the state before segment j (j = nseg: after the last),
-// rst[j] the gradient of the state after segment j.  A thread has one element of one pair's
-// states; the segments' values and decays do not depend on each other's, so their loads run
-// ahead of the sums.
-__global__ void __launch_bounds__(THREADS) gated_join(float* fst, const float* s0, float* rst, const float* ds1,
-                                                      const float* dec, int nseg, int DD) {
+// rst[j] the gradient of the state after segment j.  A workgroup has 64 elements of one
+// pair's states, each of its waves a run of up to JOIN_RUN segments of them: all of a run's
+// loads are in flight at once, the runs are joined through LDS.
+constexpr int JOIN_WAVES = 16, JOIN_RUN = 16;
+__global__ void __launch_bounds__(64 * JOIN_WAVES) gated_join(float* fst, const float* s0, float* rst, const float* ds1,
+                                                             const float* dec, int nseg, int DD) {
+    __shared__ float sums[JOIN_WAVES][64];
+    __shared__ float decays[JOIN_WAVES];
     const int64_t pair = blockIdx.y;
-    const int i = blockIdx.x * THREADS + threadIdx.x;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6, lane = threadIdx.x & 63;
+    const bool rev = (int)blockIdx.x * 64 >= DD;     // backwards segment nseg - 1 comes first
+    const int i = blockIdx.x * 64 - (rev ? DD : 0) + lane;
     const float* d = dec + pair * nseg;
-    if (i < DD) {
-        float* p = fst + pair * (nseg + 1) * DD + i;
-        float s = s0 ? s0[pair * DD + i] : 0.f;
-        p[0] = s;
-        for (int j0 = 0; j0 < nseg; j0 += 8) {
-            float loc[8], a[8];
+    const float* start = rev ? ds1 : s0;
+    float* p = rev ? rst + pair * nseg * DD + i : fst + pair * (nseg + 1) * DD + i;
+    float carry = start ? start[pair * DD + i] : 0.f;
+    // segment j's own sum lies at place j + 1 forwards and j backwards; what comes before
+    // it goes to place j
+    const int64_t own = rev ? 0 : DD;
+    for (int base = 0; base < nseg; base += waves * JOIN_RUN) {
+        const int n = min(nseg - base, waves * JOIN_RUN), per = (n + waves - 1) / waves;
+        const int k0 = wave * per, mine = min(per, n - k0);     // may be none
+        float loc[JOIN_RUN], a[JOIN_RUN];
+        float s = 0.f, prod = 1.f;
 #pragma unroll
-            for (int u = 0; u < 8; ++u) {
-                const int j = min(j0 + u, nseg - 1);
-                loc[u] = p[(int64_t)(j + 1) * DD];
+        for (int u = 0; u < JOIN_RUN; ++u) {
+            const int k = base + k0 + u, j = rev ? nseg - 1 - k : k;
+            loc[u] = 0.f;
+            a[u] = 1.f;
+            if (u < mine) {
+                loc[u] = p[(int64_t)j * DD + own];
                 a[u] = d[j];
             }
-#pragma unroll
-            for (int u = 0; u < 8; ++u)
-                if (j0 + u < nseg) {
-                    s = a[u] * s + loc[u];
-                    p[(int64_t)(j0 + u + 1) * DD] = s;
-                }
         }
-    } else if (rst && i < 2 * DD) {
-        const int e = i - DD;
-        float* p = rst + pair * nseg * DD + e;
-        float s = ds1 ? ds1[pair * DD + e] : 0.f;
-        // segment j's own sum lies at j; the state's gradient behind segment j replaces it
-        for (int j0 = nseg - 1; j0 >= 0; j0 -= 8) {
-            float loc[8], a[8];
 #pragma unroll
-            for (int u = 0; u < 8; ++u) {
-                const int j = max(j0 - u, 0);
-                loc[u] = p[(int64_t)j * DD];
-                a[u] = d[j];
+        for (int u = 0; u < JOIN_RUN; ++u) {
+            s = a[u] * s + loc[u];
+            prod *= a[u];
+        }
+        sums[wave][lane] = s;
+        if (lane == 0) decays[wave] = prod;
+        __syncthreads();                              // also: every load above is done before a store below
+        float before = carry;
+        for (int k = 0; k < waves; ++k) {
+            if (k == wave) before = carry;
+            carry = decays[k] * carry + sums[k][lane];
+        }
+#pragma unroll
+        for (int u = 0; u < JOIN_RUN; ++u) {
+            const int k = base + k0 + u, j = rev ? nseg - 1 - k : k;
+            if (u < mine) {
+                p[(int64_t)j * DD] = before;
+                before = a[u] * before + loc[u];
             }
-#pragma unroll
-            for (int u = 0; u < 8; ++u)
-                if (j0 - u >= 0) {
-                    p[(int64_t)(j0 - u) * DD] = s;
-                    s = a[u] * s + loc[u];
-                }
         }
+        __syncthreads();
     }
+    if (!rev && wave == 0) p[(int64_t)nseg * DD] = carry;
 }
 
 // ---------------------------------------------------------------- gradient of the gates
 // dg_t sums the products of pairs s < t <= t', which is
 //   sum_{t' >= t} q_t' . dq_t' - sum_{s >= t} k_s . dk_s + <S, dL/dS> at the segment's end
 // (a token's product with itself left out of both sums, where it would only cancel).  A
-// workgroup takes one segment of one (b, kv head), 256 tokens at a time from the last; the
-// sums run in 64 bits, since they cancel.  A gate of 0 passes no gradient.
+// workgroup takes one segment of one (b, kv head), up to 1024 tokens at a time from the
+// last, four a thread; the sums run in 64 bits, since they cancel.  A gate of 0 passes no
+// gradient.
 struct GateGrad {
     const float* rq;
     const float* rk;
@@ -722,56 +1131,73 @@ struct GateGrad {
     int B, T, HK, nx, nb, nseg, seg_chunks, DD;
 };
 __global__ void __launch_bounds__(THREADS) gated_gate_grad(GateGrad w) {
-    __shared__ double part[4];
+    constexpr int N = 4;
+    __shared__ double part[2][4];
     const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
-    int id = blockIdx.x;
-    const int seg = id % w.nseg;
-    id /= w.nseg;
-    const int hk = id % w.HK, b = id / w.HK;
+    int id = xcd_run(blockIdx.x, gridDim.x);
+    const int hk = id % w.HK;
+    id /= w.HK;
+    const int seg = id % w.nseg, b = id / w.nseg;
     const int64_t pair = (int64_t)b * w.HK + hk;
     const int T = w.T;
     int len = T;
     if (w.lens) len = min(max(w.lens[b], 0), T);
-    const int t0 = seg * w.seg_chunks * GC, t1 = min(t0 + w.seg_chunks * GC, T), live = min(t1, len);
+    const int t0 = seg * w.seg_chunks * GC, t1 = min(t0 + w.seg_chunks * GC, T), live = max(min(t1, len), t0);
+    const int64_t tok0 = (int64_t)b * T, tokens = (int64_t)w.B * T;
     const float* S = w.fst + (pair * (w.nseg + 1) + seg + 1) * w.DD;
     const float* R = w.rst + (pair * w.nseg + seg) * w.DD;
-    double x = 0.0;
-    for (int i = tid; i < w.DD; i += THREADS) x += (double)S[i] * (double)R[i];
+    double cross = 0.0;
+    for (int i = tid * 4; i < w.DD; i += THREADS * 4) {
+        const f32x4 s = load4(S + i), r = load4(R + i);
 #pragma unroll
-    for (int o = 1; o < 64; o <<= 1) x += __shfl_xor(x, o, 64);
-    if (lane == 0) part[wave] = x;
-    __syncthreads();
-    double carry = part[0] + part[1] + part[2] + part[3];
-    const int64_t tok0 = (int64_t)b * T;
-    for (int t = live + tid; t < t1; t += THREADS)
-        if (t >= t0) w.dg[(tok0 + t) * w.HK + hk] = 0.f;
-    for (int hi = live; hi > t0; hi -= THREADS) {
-        const int t = hi - 1 - tid;       // descending: thread 0 has the last token
-        double v = 0.0;
-        if (t >= t0) {
-            const int64_t n = (int64_t)w.B * T, tk = tok0 + t;
-            for (int e = 0; e < w.nb; ++e) {
-                for (int h = 0; h < w.nx; ++h) v += (double)w.rq[((e * n + tk) * w.HK + hk) * w.nx + h];
-                v -= (double)w.rk[(e * n + tk) * w.HK + hk];
+        for (int j = 0; j < 4; ++j) cross += (double)s[j] * (double)r[j];
+    }
+    for (int t = live + tid; t < t1; t += THREADS) w.dg[(tok0 + t) * w.HK + hk] = 0.f;
+    double carry = 0.0;
+    bool first = true;
+    for (int hi = live; hi > t0; hi -= THREADS * N) {
+        double v[N];
+        float gate[N];
+        double sum = 0.0;
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            const int t = hi - 1 - tid * N - n;       // descending: thread 0 has the last tokens
+            v[n] = 0.0;
+            gate[n] = 0.f;
+            if (t >= t0) {
+                const int64_t tk = tok0 + t;
+                gate[n] = w.g[tk * w.HK + hk];
+                for (int e = 0; e < w.nb; ++e) {
+                    for (int h = 0; h < w.nx; ++h) v[n] += (double)w.rq[((e * tokens + tk) * w.HK + hk) * w.nx + h];
+                    v[n] -= (double)w.rk[(e * tokens + tk) * w.HK + hk];
+                }
             }
+            sum += v[n];
+            v[n] = sum;
         }
+        double s = sum;
 #pragma unroll
         for (int o = 1; o < 64; o <<= 1) {
-            const double u = __shfl_up(v, o, 64);
-            if (lane >= o) v += u;
+            const double u = __shfl_up(s, o, 64);
+            if (lane >= o) s += u;
+            if (first) cross += __shfl_xor(cross, o, 64);
         }
-        __syncthreads();                  // part is free
-        if (lane == 63) part[wave] = v;
+        __syncthreads();                              // part is free
+        if (lane == 63) part[0][wave] = s;
+        if (first && lane == 0) part[1][wave] = cross;
         __syncthreads();
-        double before = carry;
+        if (first) carry = (part[1][0] + part[1][1]) + (part[1][2] + part[1][3]);
+        first = false;
+        double before = carry + s - sum;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            before += k < wave ? part[k] : 0.0;
-            carry += part[k];
+            before += k < wave ? part[0][k] : 0.0;
+            carry += part[0][k];
         }
-        if (t >= t0) {
-            const float gate = w.g[(tok0 + t) * w.HK + hk];
-            w.dg[(tok0 + t) * w.HK + hk] = gate < -104.f ? 0.f : (float)(before + v);
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            const int t = hi - 1 - tid * N - n;
+            if (t >= t0) w.dg[(tok0 + t) * w.HK + hk] = gate[n] < -104.f ? 0.f : (float)(before + v[n]);
         }
     }
 }
@@ -893,12 +1319,12 @@ hipError_t launch_local(const Local& w, hipStream_t stream) {
 
 hipError_t launch_join(float* fst, const float* s0, float* rst, const float* ds1, const float* dec, int pairs, int nseg,
                        int DD, hipStream_t stream) {
-    const int n = DD * (rst ? 2 : 1);
+    const int n = DD * (rst ? 2 : 1) / 64, waves = nseg <= 8 ? 1 : nseg < 8 * JOIN_WAVES ? (nseg + 7) / 8 : JOIN_WAVES;
     // grid.y is at most 65535: pairs are taken in runs
     for (int p = 0; p < pairs; p += 65535) {
         const int64_t o = p;
         const int m = pairs - p < 65535 ? pairs - p : 65535;
-        gated_join<<<dim3((n + THREADS - 1) / THREADS, m), THREADS, 0, stream>>>(
+        gated_join<<<dim3(n, m), 64 * waves, 0, stream>>>(
             fst + o * (nseg + 1) * DD, s0 ? s0 + o * DD : nullptr, rst ? rst + o * nseg * DD : nullptr,
             ds1 ? ds1 + o * DD : nullptr, dec + o * nseg, nseg, DD);
     }
@@ -992,31 +1418,50 @@ hipError_t backward(const GatedBackward& f) {
     w.pair_scale = w.row_scale = p.scale;
     w.key_scale = 1.f;
     if ((err = launch_walk<E, D, false, true>(w, p.stream)) != hipSuccess) return err;
-    // dv, and the initial state's gradient
-    w.x = {p.k, p.ks};
-    w.y = {p.q, p.qs};
-    w.z = {f.dout, hs};
-    w.x2 = {nullptr, 0};
-    w.out = f.dv;
-    w.r = nullptr;
-    w.start = f.rst;
-    w.start_pair = (int64_t)p.nseg * DD;
-    w.end = f.ds0;
-    w.sc = D; w.se = 1;
-    w.nx = 1; w.ny = G;
-    w.row_scale = 1.f;
-    w.key_scale = p.scale;
-    if ((err = launch_walk<E, D, true, false>(w, p.stream)) != hipSuccess) return err;
-    // dk and k . dk
-    w.x = {p.v, p.vs};
-    w.y = {f.dout, hs};
-    w.z = {p.q, p.qs};
-    w.x2 = {p.k, p.ks};
-    w.out = f.dk;
-    w.r = f.rk;
-    w.end = nullptr;
-    w.sc = 1; w.se = D;
-    if ((err = launch_walk<E, D, true, true>(w, p.stream)) != hipSuccess) return err;
+    if constexpr (D <= 64) {
+        Back k = {};
+        k.q = {p.q, p.qs};
+        k.k = {p.k, p.ks};
+        k.v = {p.v, p.vs};
+        k.dout = {f.dout, hs};
+        k.dk = f.dk;
+        k.dv = f.dv;
+        k.r = f.rk;
+        k.g = p.g;
+        k.lens = p.lens;
+        k.start = f.rst;
+        k.end = f.ds0;
+        k.B = p.B; k.T = p.T; k.HK = p.HK; k.G = G; k.nseg = p.nseg; k.seg_chunks = p.seg_chunks;
+        k.scale = p.scale;
+        gated_back<E, D><<<dim3((unsigned)((int64_t)p.B * p.HK * p.nseg)), THREADS, 0, p.stream>>>(k);
+        if ((err = hipGetLastError()) != hipSuccess) return err;
+    } else {
+        // dv, and the initial state's gradient
+        w.x = {p.k, p.ks};
+        w.y = {p.q, p.qs};
+        w.z = {f.dout, hs};
+        w.x2 = {nullptr, 0};
+        w.out = f.dv;
+        w.r = nullptr;
+        w.start = f.rst;
+        w.start_pair = (int64_t)p.nseg * DD;
+        w.end = f.ds0;
+        w.sc = D; w.se = 1;
+        w.nx = 1; w.ny = G;
+        w.row_scale = 1.f;
+        w.key_scale = p.scale;
+        if ((err = launch_walk<E, D, true, false>(w, p.stream)) != hipSuccess) return err;
+        // dk and k . dk
+        w.x = {p.v, p.vs};
+        w.y = {f.dout, hs};
+        w.z = {p.q, p.qs};
+        w.x2 = {p.k, p.ks};
+        w.out = f.dk;
+        w.r = f.rk;
+        w.end = nullptr;
+        w.sc = 1; w.se = D;
+        if ((err = launch_walk<E, D, true, true>(w, p.stream)) != hipSuccess) return err;
+    }
 
     GateGrad d;
     d.rq = f.rq; d.rk = f.rk; d.fst = f.fst; d.rst = f.rst; d.g = p.g; d.lens = p.lens; d.dg = f.dg;

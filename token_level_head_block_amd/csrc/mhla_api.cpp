@@ -908,16 +908,19 @@ mhla_status check_seq(const mhla_seq* q, Seq* s, bool groups) {
         *out[i] = in[i] == 0 ? least[i] : in[i];
         if (*out[i] < least[i]) return MHLA_ERR_INVALID_ARG;
         if (*out[i] * (int64_t)s->esz % 16 != 0) return MHLA_ERR_MISALIGNED;
-        if (*out[i] > ((int64_t)1 << 40)) return MHLA_ERR_UNSUPPORTED;
+        if (*out[i] > (1 << 23)) return MHLA_ERR_UNSUPPORTED;   // the kernels' 32-bit offsets in a chunk of 64 tokens
         // every tensor's bytes stay within 2^62
         if ((double)s->B * (double)s->T * (double)*out[i] * 4.0 > 4.6e18) return MHLA_ERR_UNSUPPORTED;
     }
     return MHLA_OK;
 }
 
-// Segments of a sequence: workgroups walk them side by side.  One more segment costs a pass
-// over its keys and values and a state written and read, so a sequence is split only while
-// there are fewer than WALKS walks, and not into segments of fewer than LEAST chunks.
+// Segments of a sequence: workgroups walk them side by side, at most as many as the compute
+// units hold at once (256 of them: the plan fixes the workspace, so it goes by the problem
+// alone).  A few more would run as a second round, as long as the first: dit-s2-256x256 as
+// one sequence, forwards 81 us with 768 walks, 96 with 1024, 93 with 512; backwards 234 us
+// with 512, 254 with 1024.  Short sequences are split down to single chunks, which shortens
+// the longest walk (4 x 1000 tokens, head_dim 128: 31 us against 48 with four chunks a walk).
 // Backwards, segments of at most MOST chunks: the gates' gradients start anew from <S, dS>
 // at each segment's end.
 struct GatedPlan {
@@ -925,11 +928,11 @@ struct GatedPlan {
     size_t fst, rst, dec, rq, rk, total;
 };
 GatedPlan gated_plan(const Seq& s, bool backward) {
-    constexpr int64_t WALKS = 1024, LEAST = 4, MOST = 16;
+    constexpr int64_t CUS = 256, MOST = 16;
     const int64_t C = mhla::GATED_CHUNK, chunks = s.T > 0 ? (s.T + C - 1) / C : 1;
     const int64_t walks = s.B * s.HK * mhla::gated_value_blocks((int)s.D);
-    int64_t n = (WALKS + walks - 1) / walks;
-    if (n > (chunks + LEAST - 1) / LEAST) n = (chunks + LEAST - 1) / LEAST;
+    int64_t n = CUS * mhla::gated_walks_per_cu(s.esz == 2, (int)s.D, backward) / walks;
+    if (n > chunks) n = chunks;
     if (backward && n < (chunks + MOST - 1) / MOST) n = (chunks + MOST - 1) / MOST;
     if (n < 1) n = 1;
     GatedPlan p;
