@@ -473,15 +473,16 @@ def _need(name, t, shape, dtype, device):
 
 
 def _stride_of(name, t, shape, dtype, device):
-    """Values between a token of t and the next one, for a tensor [B, T, heads, d] whose tokens' values
-    are contiguous and evenly spaced over the whole batch (a slice of a wider row, say)."""
+    """Values between a token of t and the next one, for a tensor [B, T, heads, d] (or rows [B, heads, d])
+    whose tokens' values are contiguous and evenly spaced over the whole batch (a slice of a wider row, say)."""
     if t.shape != shape or t.dtype != dtype or t.device != device:
         raise ValueError(f"{name} must be a {dtype} tensor of shape {tuple(shape)} on {device}, "
                          f"got {t.dtype} {tuple(t.shape)} on {t.device}")
-    B, T, h, d = shape
+    h, d = shape[-2:]
     if t.is_contiguous():
         return h * d
-    sb, st, sh, sd = t.stride()
+    B, T = shape[0], shape[1] if len(shape) == 4 else 1
+    sb, st, (sh, sd) = t.stride(0), t.stride(1) if len(shape) == 4 else 0, t.stride()[-2:]
     step = st if T > 1 else sb if B > 1 else h * d
     if sd != 1 or (h > 1 and sh != d) or (T > 1 and B > 1 and sb != T * st) or step < h * d:
         raise ValueError(f"{name}: the values of a token must be contiguous and tokens evenly spaced, "
@@ -489,9 +490,9 @@ def _stride_of(name, t, shape, dtype, device):
     return step
 
 
-def _check_seq_tensors(q, k, v, seq: mhla_seq):
-    """The type and device of a sequence problem's tensors, after checking q, k and v (or None) against seq.
-    The C ABI cannot see tensor sizes."""
+def _check_seq_tensors(q, k, v, seq: mhla_seq, rows: bool = False):
+    """The type and device of a sequence problem's tensors, after checking q, k and v (or None) against seq
+    (rows: [B, heads, d], one token each).  The C ABI cannot see tensor sizes."""
     import torch
     dt = torch.bfloat16 if seq.dtype == MHLA_BF16 else torch.float32
     dev = q.device
@@ -501,7 +502,7 @@ def _check_seq_tensors(q, k, v, seq: mhla_seq):
     for name, t, h, stride in (("q", q, H, seq.q_stride), ("k", k, Hk, seq.k_stride), ("v", v, Hk, seq.v_stride)):
         if t is None:
             continue
-        s = _stride_of(name, t, (B, T, h, d), dt, dev)
+        s = _stride_of(name, t, (B, h, d) if rows else (B, T, h, d), dt, dev)
         if B * T > 1 and s != (stride or h * d):
             raise ValueError(f"{name}: a token stride of {s} where seq has {stride or h * d}")
     return dt, dev
@@ -526,20 +527,26 @@ def _call(fn, device, stream, *args) -> int:
         return fn(*args, s)
 
 
+def _check_gated(seq, dt, dev, g, lens, states, **tensors):
+    """g [B, T, Hk], lens and states (name: tensor or None) and, by name, tensors with their head counts."""
+    import torch
+    B, T, Hk, d = seq.batch, seq.tokens, seq.kv_heads, seq.head_dim
+    _need("g", g, (B, T, Hk), torch.float32, dev)
+    if lens is not None:
+        _need("lens", lens, (B,), torch.int32, dev)
+    for name, t in states.items():
+        if t is not None:
+            _need(name, t, (B, Hk, d, d), torch.float32, dev)
+    for name, (t, h) in tensors.items():
+        _need(name, t, (B, T, h, d), dt, dev)
+
+
 def mhla_gated_forward(q, k, v, g, seq: mhla_seq, out, lens=None, state=None, state_out=None, ws=None,
                        ws_bytes: int = 0, stream=None) -> int:
     """The C entry point with torch tensors: q, out [B, T, H, d], k, v [B, T, Hk, d], g fp32 [B, T, Hk],
     lens int32 [B] or None, state and state_out fp32 [B, Hk, d, d] or None."""
-    import torch
     dt, dev = _check_seq_tensors(q, k, v, seq)
-    B, T, H, Hk, d = seq.batch, seq.tokens, seq.heads, seq.kv_heads, seq.head_dim
-    _need("g", g, (B, T, Hk), torch.float32, dev)
-    _need("out", out, (B, T, H, d), dt, dev)
-    if lens is not None:
-        _need("lens", lens, (B,), torch.int32, dev)
-    for name, t in (("state", state), ("state_out", state_out)):
-        if t is not None:
-            _need(name, t, (B, Hk, d, d), torch.float32, dev)
+    _check_gated(seq, dt, dev, g, lens, {"state": state, "state_out": state_out}, out=(out, seq.heads))
     _check_workspace(ws, ws_bytes, dev)
     return _call(lib().mhla_gated_forward, dev, stream, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(lens), _ptr(state),
                  ctypes.byref(seq), _ptr(out), _ptr(state_out), _ptr(ws), ws_bytes)
@@ -551,57 +558,52 @@ def mhla_gated_backward(q, k, v, g, dout, seq: mhla_seq, dq, dk, dv, dg, lens=No
     final state's gradient (or None), dstate receives the initial state's (or None)."""
     import torch
     dt, dev = _check_seq_tensors(q, k, v, seq)
-    B, T, H, Hk, d = seq.batch, seq.tokens, seq.heads, seq.kv_heads, seq.head_dim
-    for name, t in (("dout", dout), ("dq", dq)):
-        _need(name, t, (B, T, H, d), dt, dev)
-    for name, t in (("dk", dk), ("dv", dv)):
-        _need(name, t, (B, T, Hk, d), dt, dev)
-    for name, t in (("g", g), ("dg", dg)):
-        _need(name, t, (B, T, Hk), torch.float32, dev)
-    if lens is not None:
-        _need("lens", lens, (B,), torch.int32, dev)
-    for name, t in (("state", state), ("dstate_out", dstate_out), ("dstate", dstate)):
-        if t is not None:
-            _need(name, t, (B, Hk, d, d), torch.float32, dev)
+    H, Hk = seq.heads, seq.kv_heads
+    _check_gated(seq, dt, dev, g, lens, {"state": state, "dstate_out": dstate_out, "dstate": dstate}, dout=(dout, H),
+                 dq=(dq, H), dk=(dk, Hk), dv=(dv, Hk))
+    _need("dg", dg, g.shape, torch.float32, dev)
     _check_workspace(ws, ws_bytes, dev)
     return _call(lib().mhla_gated_backward, dev, stream, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(lens), _ptr(state),
                  _ptr(dout), _ptr(dstate_out), ctypes.byref(seq), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dg),
                  _ptr(dstate), _ptr(ws), ws_bytes)
 
 
+def _check_step(seq, dev, g, state, slots):
+    import torch
+    B, Hk, d = seq.batch, seq.kv_heads, seq.head_dim
+    n = state.shape[0]
+    _need("g", g, (B, Hk), torch.float32, dev)
+    _need("state", state, (n, Hk, d, d), torch.float32, dev)
+    if slots is not None:
+        _need("slots", slots, (B,), torch.int32, dev)
+    return n
+
+
 def mhla_gated_step(q, k, v, g, seq: mhla_seq, state, out, slots=None, stream=None) -> int:
     """One token a row: q, out [B, H, d], k, v [B, Hk, d], g fp32 [B, Hk], state fp32 [num_slots, Hk, d, d]
     (updated in place), slots int32 [B] or None (row b has entry b)."""
-    import torch
-    dt, dev = _check_seq_tensors(q.unsqueeze(1), k.unsqueeze(1), v.unsqueeze(1), seq)
-    B, H, Hk, d = seq.batch, seq.heads, seq.kv_heads, seq.head_dim
-    _need("g", g, (B, Hk), torch.float32, dev)
-    _need("out", out, (B, H, d), dt, dev)
-    if slots is not None:
-        _need("slots", slots, (B,), torch.int32, dev)
-    n = state.shape[0]
-    _need("state", state, (n, Hk, d, d), torch.float32, dev)
+    dt, dev = _check_seq_tensors(q, k, v, seq, rows=True)
+    n = _check_step(seq, dev, g, state, slots)
+    _need("out", out, (seq.batch, seq.heads, seq.head_dim), dt, dev)
     return _call(lib().mhla_gated_step, dev, stream, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(slots),
                  ctypes.byref(seq), _ptr(state), n, _ptr(out))
 
 
-def _check_rope_tensors(q, k, w_q, w_k, positions, freq, rope: mhla_rope, seq: mhla_seq):
+def _check_rope_tensors(w_q, w_k, positions, freq, rope: mhla_rope, seq: mhla_seq, dev):
     import torch
-    dt, dev = _check_seq_tensors(q, k, None, seq)
-    d = seq.head_dim
     _need("positions", positions, (seq.batch, seq.tokens, rope.axes), torch.int32, dev)
-    _need("freq", freq, (rope.section[0] + rope.section[1] + rope.section[2],), torch.float32, dev)
+    _need("freq", freq, (sum(rope.section),), torch.float32, dev)
     for name, t in (("w_q", w_q), ("w_k", w_k)):
         if t is not None:
-            _need(name, t, (d,), torch.float32, dev)
-    return dt, dev
+            _need(name, t, (seq.head_dim,), torch.float32, dev)
 
 
 def mhla_qk_norm_rope(q, k, w_q, w_k, positions, freq, rope: mhla_rope, seq: mhla_seq, q_out, k_out,
                       stream=None) -> int:
     """q, q_out [B, T, H, d], k, k_out [B, T, Hk, d], w_q, w_k fp32 [d] or None, positions int32 [B, T, axes],
     freq fp32 [pairs]."""
-    dt, dev = _check_rope_tensors(q, k, w_q, w_k, positions, freq, rope, seq)
+    dt, dev = _check_seq_tensors(q, k, None, seq)
+    _check_rope_tensors(w_q, w_k, positions, freq, rope, seq, dev)
     _need("q_out", q_out, q.shape, dt, dev)
     _need("k_out", k_out, k.shape, dt, dev)
     return _call(lib().mhla_qk_norm_rope, dev, stream, _ptr(q), _ptr(k), _ptr(w_q), _ptr(w_k), _ptr(positions),
@@ -612,7 +614,8 @@ def mhla_qk_norm_rope_backward(q, k, w_q, w_k, positions, freq, rope: mhla_rope,
                                dk, dw_q=None, dw_k=None, ws=None, ws_bytes: int = 0, stream=None) -> int:
     """Gradients through mhla_qk_norm_rope; dw_q, dw_k fp32 [d] or None."""
     import torch
-    dt, dev = _check_rope_tensors(q, k, w_q, w_k, positions, freq, rope, seq)
+    dt, dev = _check_seq_tensors(q, k, None, seq)
+    _check_rope_tensors(w_q, w_k, positions, freq, rope, seq, dev)
     for name, t, like in (("dq_out", dq_out, q), ("dq", dq, q), ("dk_out", dk_out, k), ("dk", dk, k)):
         _need(name, t, like.shape, dt, dev)
     for name, t in (("dw_q", dw_q), ("dw_k", dw_k)):
@@ -624,24 +627,33 @@ def mhla_qk_norm_rope_backward(q, k, w_q, w_k, positions, freq, rope: mhla_rope,
                  _ptr(dq), _ptr(dk), _ptr(dw_q), _ptr(dw_k), _ptr(ws), ws_bytes)
 
 
-def _seq_of(q, k, v, scale=None) -> mhla_seq:
-    """The sequence problem of tensors q [B, T, H, d], k and v [B, T, Hk, d] (v or None)."""
+def _seq_of(q, k, v, scale=None, rows: bool = False):
+    """The sequence problem of tensors q [B, T, H, d], k and v [B, T, Hk, d] (v or None; rows: without T, one
+    token each), checked against each other, and their device."""
     import torch
-    if q.dim() != 4 or k.dim() != 4:
-        raise ValueError("q, k and v must be [batch, tokens, heads, head_dim]")
-    dt = {torch.bfloat16: MHLA_BF16, torch.float32: MHLA_F32}.get(q.dtype)
+    n = 3 if rows else 4
+    if q.dim() != n or k.dim() != n:
+        raise ValueError("q, k and v must be [batch, heads, head_dim]" if rows else
+                         "q, k and v must be [batch, tokens, heads, head_dim]")
+    t, dev = q.dtype, q.device
+    dt = MHLA_BF16 if t == torch.bfloat16 else MHLA_F32 if t == torch.float32 else None
     if dt is None:
-        raise ValueError(f"q must be bfloat16 or float32, got {q.dtype}")
-    B, T, H, d = q.shape
-    Hk = k.shape[2]
-    strides = [_stride_of(n, t, (B, T, h, d), q.dtype, q.device) if t is not None else 0
-               for n, t, h in (("q", q, H), ("k", k, Hk), ("v", v, Hk))]
-    return make_seq(B, T, H, Hk, d, dt, d ** -0.5 if scale is None else scale, *strides)
+        raise ValueError(f"q must be bfloat16 or float32, got {t}")
+    shape = q.shape
+    H, d = shape[-2], shape[-1]
+    Hk = k.shape[-2]
+    kv = (*shape[:-2], Hk, d)
+    qs, ks = _stride_of("q", q, shape, t, dev), _stride_of("k", k, kv, t, dev)
+    vs = 0 if v is None else _stride_of("v", v, kv, t, dev)
+    if dev.type != "cuda":
+        raise ValueError("q must be on a GPU")
+    return mhla_seq(shape[0], 1 if rows else shape[1], H, Hk, d, dt, qs, ks, vs,
+                    d ** -0.5 if scale is None else scale), dev
 
 
-def _workspace(n, like):
+def _workspace(n, device):
     import torch
-    return torch.empty(n, dtype=torch.uint8, device=like.device) if n else None
+    return torch.empty(n, dtype=torch.uint8, device=device) if n else None
 
 
 def _raise(st, what):
@@ -654,13 +666,16 @@ def gated_forward(q, k, v, g, scale=None, state=None, lens=None, want_state: boo
     (scale: head_dim ** -0.5 by default).  Returns out, and with want_state (out, the final state).  Runs on the
     current stream of the tensors' device; tensors as for mhla_gated_forward."""
     import torch
-    seq = _seq_of(q, k, v, scale)
-    out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    seq, dev = _seq_of(q, k, v, scale)
+    _check_gated(seq, q.dtype, dev, g, lens, {"state": state})
+    out = q.new_empty(q.shape)
     new = None
     if want_state:
-        new = torch.empty(seq.batch, seq.kv_heads, seq.head_dim, seq.head_dim, dtype=torch.float32, device=q.device)
+        new = torch.empty(seq.batch, seq.kv_heads, seq.head_dim, seq.head_dim, dtype=torch.float32, device=dev)
     n = mhla_gated_workspace_bytes(seq)
-    _raise(mhla_gated_forward(q, k, v, g, seq, out, lens, state, new, _workspace(n, q), n), "mhla_gated_forward")
+    ws = _workspace(n, dev)
+    _raise(_call(lib().mhla_gated_forward, dev, None, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(lens), _ptr(state),
+                 ctypes.byref(seq), _ptr(out), _ptr(new), _ptr(ws), n), "mhla_gated_forward")
     return (out, new) if want_state else out
 
 
@@ -668,34 +683,40 @@ def gated_backward(q, k, v, g, dout, scale=None, state=None, dstate=None, lens=N
     """(dq, dk, dv, dg, gradient of the initial state) of gated_forward, given dout and, if not None, dstate, the
     final state's gradient.  The last one is None where state is."""
     import torch
-    seq = _seq_of(q, k, v, scale)
-    dq, dk, dv = (torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q, k, v))
+    seq, dev = _seq_of(q, k, v, scale)
+    _check_gated(seq, q.dtype, dev, g, lens, {"state": state, "dstate": dstate}, dout=(dout, seq.heads))
+    dq, dk, dv = (t.new_empty(t.shape) for t in (q, k, v))
     dg = torch.empty_like(g)
     dstart = None if state is None else torch.empty_like(state)
     n = mhla_gated_backward_workspace_bytes(seq)
-    _raise(mhla_gated_backward(q, k, v, g, dout, seq, dq, dk, dv, dg, lens, state, dstate, dstart, _workspace(n, q),
-                               n), "mhla_gated_backward")
+    ws = _workspace(n, dev)
+    _raise(_call(lib().mhla_gated_backward, dev, None, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(lens), _ptr(state),
+                 _ptr(dout), _ptr(dstate), ctypes.byref(seq), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dg), _ptr(dstart),
+                 _ptr(ws), n), "mhla_gated_backward")
     return dq, dk, dv, dg, dstart
 
 
 def gated_step(q, k, v, g, state, scale=None, slots=None):
     """One token for each row: q [B, H, d], k, v [B, Hk, d], g [B, Hk]; state [num_slots, Hk, d, d] is updated in
     place.  Returns out [B, H, d].  slots as for mhla_gated_step."""
-    import torch
-    seq = _seq_of(q.unsqueeze(1), k.unsqueeze(1), v.unsqueeze(1), scale)
-    out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    _raise(mhla_gated_step(q, k, v, g, seq, state, out, slots), "mhla_gated_step")
+    seq, dev = _seq_of(q, k, v, scale, rows=True)
+    n = _check_step(seq, dev, g, state, slots)
+    out = q.new_empty(q.shape)
+    _raise(_call(lib().mhla_gated_step, dev, None, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(slots),
+                 ctypes.byref(seq), _ptr(state), n, _ptr(out)), "mhla_gated_step")
     return out
 
 
 def qk_norm_rope(q, k, w_q, w_k, positions, freq, sections=None, style: int = MHLA_ROPE_HALVES, eps: float = 1e-6):
     """RMSNorm of every head of q and k with weights w_q, w_k (or None), and the rotation by the tokens'
     positions.  sections: pairs of each axis (one axis for all of freq by default).  Returns (q, k)."""
-    import torch
-    seq = _seq_of(q, k, None, 1.0)
+    seq, dev = _seq_of(q, k, None, 1.0)
     rope = make_rope(sections if sections is not None else (freq.numel(),), style, eps)
-    qo, ko = (torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q, k))
-    _raise(mhla_qk_norm_rope(q, k, w_q, w_k, positions, freq, rope, seq, qo, ko), "mhla_qk_norm_rope")
+    _check_rope_tensors(w_q, w_k, positions, freq, rope, seq, dev)
+    qo = q.new_empty(q.shape)
+    ko = k.new_empty(k.shape)
+    _raise(_call(lib().mhla_qk_norm_rope, dev, None, _ptr(q), _ptr(k), _ptr(w_q), _ptr(w_k), _ptr(positions),
+                 _ptr(freq), ctypes.byref(rope), ctypes.byref(seq), _ptr(qo), _ptr(ko)), "mhla_qk_norm_rope")
     return qo, ko
 
 
@@ -703,11 +724,17 @@ def qk_norm_rope_backward(q, k, w_q, w_k, positions, freq, sections, dq_out, dk_
                           eps: float = 1e-6):
     """(dq, dk, dw_q, dw_k) of qk_norm_rope; a weight's gradient is None where the weight is."""
     import torch
-    seq = _seq_of(q, k, None, 1.0)
+    seq, dev = _seq_of(q, k, None, 1.0)
     rope = make_rope(sections if sections is not None else (freq.numel(),), style, eps)
-    dq, dk = (torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q, k))
-    dw = [None if w is None else torch.empty_like(w) for w in (w_q, w_k)]
+    _check_rope_tensors(w_q, w_k, positions, freq, rope, seq, dev)
+    _need("dq_out", dq_out, q.shape, q.dtype, dev)
+    _need("dk_out", dk_out, k.shape, k.dtype, dev)
+    dq = q.new_empty(q.shape)
+    dk = k.new_empty(k.shape)
+    dwq, dwk = (None if w is None else torch.empty_like(w) for w in (w_q, w_k))
     n = mhla_qk_norm_rope_backward_workspace_bytes(seq)
-    _raise(mhla_qk_norm_rope_backward(q, k, w_q, w_k, positions, freq, rope, dq_out, dk_out, seq, dq, dk, *dw,
-                                      _workspace(n, q), n), "mhla_qk_norm_rope_backward")
-    return dq, dk, *dw
+    ws = _workspace(n, dev)
+    _raise(_call(lib().mhla_qk_norm_rope_backward, dev, None, _ptr(q), _ptr(k), _ptr(w_q), _ptr(w_k), _ptr(positions),
+                 _ptr(freq), ctypes.byref(rope), _ptr(dq_out), _ptr(dk_out), ctypes.byref(seq), _ptr(dq), _ptr(dk),
+                 _ptr(dwq), _ptr(dwk), _ptr(ws), n), "mhla_qk_norm_rope_backward")
+    return dq, dk, dwq, dwk

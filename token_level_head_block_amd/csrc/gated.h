@@ -9,6 +9,8 @@ namespace mhla {
 
 // Tokens of a chunk (one wave holds a chunk's gates, a token a lane).
 constexpr int GATED_CHUNK = 64;
+// Chunks of a segment at most, backwards (the gates' gradients hold a segment's tokens).
+constexpr int GATED_MAX_CHUNKS = 16;
 
 // One sequence problem with the caller's device pointers.  Strides are in
 // elements between a token and the next; a batch item is T tokens.

@@ -117,8 +117,11 @@ struct Tile {
     __device__ static __forceinline__ int at(int row, int piece) {
         int f;
         if constexpr (sizeof(E) == 2) {
-            const int m = (row / RP) & (NP - 1);
-            f = ((m & (NP / 2 - 1)) << 1) | (m / (NP / 2));
+            // 16-byte reads of one piece run over rows 0-3, 12-15 of it and 4-11 of the next piece
+            // together, transposing reads over 8 rows of two neighbouring pieces
+            constexpr int H = NP / 2;
+            const int m = (row / RP) & (NP - 1), up = m / H;
+            f = (((m & (H - 1)) ^ (up * (H / 2))) << 1) | up;
         } else {
             f = (row / RP) & ((NP < 16 ? NP : 16) - 1);
         }
@@ -574,11 +577,12 @@ __global__ void __launch_bounds__(THREADS, sizeof(E) == 2 || D <= 64 ? 2 : 1) ga
     fetch(0, 0);
     fetch_x(0, 0, xf, x2f);
 
+    const bool keep = w.end && (REV ? seg == 0 : seg == w.nseg - 1);   // the state after the last chunk is wanted
     f32x4 o[ET];
     float rsum = 0.f;
     for (int ci = 0; ci < chunks; ++ci) {
         const int c = first + dir * ci;
-        const bool live = c * GC + tl < len;
+        const bool live = c * GC + tl < len, whole = (c + 1) * GC <= len;
         const int rows = min(T - c * GC, GC);
         const int64_t tk0 = tok0 + (int64_t)c * GC;
         const Gates gs = gate_sums(graw);
@@ -693,10 +697,14 @@ __global__ void __launch_bounds__(THREADS, sizeof(E) == 2 || D <= 64 ? 2 : 1) ga
                 if (!REV || last_y) {
                     const int h = hk * nx + hx;
                     const __amdgpu_buffer_rsrc_t ro = rows_of<E>(w.out, tk0, (int64_t)hx_all * D, h * D + eb * EB, rows, EB);
-                    const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+                    if (!whole) {
+#pragma unroll
+                        for (int e = 0; e < ET; ++e)
+                            if (!live) o[e] = f32x4{0.f, 0.f, 0.f, 0.f};
+                    }
 #pragma unroll
                     for (int e = 0; e < ET; ++e)
-                        store_row4(ro, (tl * hx_all * D + 16 * e + 4 * lg) * ES, live ? o[e] : zero, E());
+                        store_row4(ro, (tl * hx_all * D + 16 * e + 4 * lg) * ES, o[e], E());
                     if constexpr (DOT) {
                         float s = rsum + shfl_xor(rsum, 16);
                         s += shfl_xor(s, 32);     // all four lanes of a token store the same sum
@@ -711,11 +719,11 @@ __global__ void __launch_bounds__(THREADS, sizeof(E) == 2 || D <= 64 ? 2 : 1) ga
                     }
                 }
             }
-            update_state<E, D, EB>(S, yt, zt, kw, decay, wave, lane);
+            if (keep || ci + 1 < chunks) update_state<E, D, EB>(S, yt, zt, kw, decay, wave, lane);
             decay = 1.f;
         }
     }
-    if (w.end && (REV ? seg == 0 : seg == w.nseg - 1))
+    if (keep)
         store_state<D, EB>(S, w.end + ((int64_t)b * w.HK + hk) * D * D + eb * EB * w.se, w.sc, w.se, wave, lane);
 }
 
@@ -814,11 +822,12 @@ __global__ void __launch_bounds__(THREADS, sizeof(E) == 2 || D == 32 ? 2 : 1) ga
     fetch(0, 0);
     fetch_x(0, kf, vf);
 
+    const bool keep = w.end && seg == 0;
     f32x4 ok[DT], ov[DT];
     float rsum = 0.f;
     for (int ci = 0; ci < chunks; ++ci) {
         const int c = live_end - 1 - ci;
-        const bool live = c * GC + tl < len;
+        const bool live = c * GC + tl < len, whole = (c + 1) * GC <= len;
         const int rows = min(T - c * GC, GC);
         const int64_t tk0 = tok0 + (int64_t)c * GC;
         const Gates gs = gate_sums(graw);
@@ -933,19 +942,23 @@ __global__ void __launch_bounds__(THREADS, sizeof(E) == 2 || D == 32 ? 2 : 1) ga
             if (last) {
                 const __amdgpu_buffer_rsrc_t rv = rows_of<E>(w.dv, tk0, (int64_t)w.HK * D, hk * D, rows, D);
                 const __amdgpu_buffer_rsrc_t rk = rows_of<E>(w.dk, tk0, (int64_t)w.HK * D, hk * D, rows, D);
-                const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+                if (!whole) {
+#pragma unroll
+                    for (int e = 0; e < DT; ++e)
+                        if (!live) ov[e] = ok[e] = f32x4{0.f, 0.f, 0.f, 0.f};
+                }
 #pragma unroll
                 for (int e = 0; e < DT; ++e) {
                     const int off = (tl * w.HK * D + 16 * e + 4 * lg) * ES;
-                    store_row4(rv, off, live ? ov[e] : zero, E());
-                    store_row4(rk, off, live ? ok[e] : zero, E());
+                    store_row4(rv, off, ov[e], E());
+                    store_row4(rk, off, ok[e], E());
                 }
                 float s = rsum + shfl_xor(rsum, 16);
                 s += shfl_xor(s, 32);             // all four lanes of a token store the same sum
                 __builtin_amdgcn_raw_buffer_store_b32(__float_as_int(live ? s : 0.f), rows_of<float>(w.r, tk0, w.HK, hk, rows, 1),
                                                       tl * w.HK * 4, 0, 0);
             }
-            update_state<E, D, D>(S, yt, zt, kw, decay, wave, lane);
+            if (keep || ci + 1 < chunks) update_state<E, D, D>(S, yt, zt, kw, decay, wave, lane);
             decay = 1.f;
         }
 #pragma unroll
@@ -954,7 +967,7 @@ __global__ void __launch_bounds__(THREADS, sizeof(E) == 2 || D == 32 ? 2 : 1) ga
             vf[kk] = vn[kk];
         }
     }
-    if (w.end && seg == 0) store_state<D, D>(S, w.end + pair * D * D, D, 1, wave, lane);
+    if (keep) store_state<D, D>(S, w.end + pair * D * D, D, 1, wave, lane);
 }
 
 // ---------------------------------------------------------------- segments
@@ -1117,9 +1130,8 @@ __global__ void __launch_bounds__(64 * JOIN_WAVES) gated_join(float* fst, const 
 // dg_t sums the products of pairs s < t <= t', which is
 //   sum_{t' >= t} q_t' . dq_t' - sum_{s >= t} k_s . dk_s + <S, dL/dS> at the segment's end
 // (a token's product with itself left out of both sums, where it would only cancel).  A
-// workgroup takes one segment of one (b, kv head), up to 1024 tokens at a time from the
-// last, four a thread; the sums run in 64 bits, since they cancel.  A gate of 0 passes no
-// gradient.
+// workgroup takes one segment of one (b, kv head): at most 16 chunks, four tokens a thread
+// from the last; the sums run in 64 bits, since they cancel.  A gate of 0 passes no gradient.
 struct GateGrad {
     const float* rq;
     const float* rk;
@@ -1131,7 +1143,7 @@ struct GateGrad {
     int B, T, HK, nx, nb, nseg, seg_chunks, DD;
 };
 __global__ void __launch_bounds__(THREADS) gated_gate_grad(GateGrad w) {
-    constexpr int N = 4;
+    constexpr int N = GATED_MAX_CHUNKS * GC / THREADS;
     __shared__ double part[2][4];
     const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
     int id = xcd_run(blockIdx.x, gridDim.x);
@@ -1144,6 +1156,24 @@ __global__ void __launch_bounds__(THREADS) gated_gate_grad(GateGrad w) {
     if (w.lens) len = min(max(w.lens[b], 0), T);
     const int t0 = seg * w.seg_chunks * GC, t1 = min(t0 + w.seg_chunks * GC, T), live = max(min(t1, len), t0);
     const int64_t tok0 = (int64_t)b * T, tokens = (int64_t)w.B * T;
+    // this thread's tokens, descending: thread 0 has the last ones
+    double v[N];
+    float gate[N];
+    double sum = 0.0;
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        const int t = live - 1 - tid * N - n;
+        v[n] = 0.0;
+        gate[n] = 0.f;
+        if (t >= t0) {
+            const int64_t tk = tok0 + t;
+            gate[n] = w.g[tk * w.HK + hk];
+            for (int e = 0; e < w.nb; ++e) {
+                for (int h = 0; h < w.nx; ++h) v[n] += (double)w.rq[((e * tokens + tk) * w.HK + hk) * w.nx + h];
+                v[n] -= (double)w.rk[(e * tokens + tk) * w.HK + hk];
+            }
+        }
+    }
     const float* S = w.fst + (pair * (w.nseg + 1) + seg + 1) * w.DD;
     const float* R = w.rst + (pair * w.nseg + seg) * w.DD;
     double cross = 0.0;
@@ -1152,54 +1182,30 @@ __global__ void __launch_bounds__(THREADS) gated_gate_grad(GateGrad w) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) cross += (double)s[j] * (double)r[j];
     }
-    for (int t = live + tid; t < t1; t += THREADS) w.dg[(tok0 + t) * w.HK + hk] = 0.f;
-    double carry = 0.0;
-    bool first = true;
-    for (int hi = live; hi > t0; hi -= THREADS * N) {
-        double v[N];
-        float gate[N];
-        double sum = 0.0;
 #pragma unroll
-        for (int n = 0; n < N; ++n) {
-            const int t = hi - 1 - tid * N - n;       // descending: thread 0 has the last tokens
-            v[n] = 0.0;
-            gate[n] = 0.f;
-            if (t >= t0) {
-                const int64_t tk = tok0 + t;
-                gate[n] = w.g[tk * w.HK + hk];
-                for (int e = 0; e < w.nb; ++e) {
-                    for (int h = 0; h < w.nx; ++h) v[n] += (double)w.rq[((e * tokens + tk) * w.HK + hk) * w.nx + h];
-                    v[n] -= (double)w.rk[(e * tokens + tk) * w.HK + hk];
-                }
-            }
-            sum += v[n];
-            v[n] = sum;
-        }
-        double s = sum;
-#pragma unroll
-        for (int o = 1; o < 64; o <<= 1) {
-            const double u = __shfl_up(s, o, 64);
-            if (lane >= o) s += u;
-            if (first) cross += __shfl_xor(cross, o, 64);
-        }
-        __syncthreads();                              // part is free
-        if (lane == 63) part[0][wave] = s;
-        if (first && lane == 0) part[1][wave] = cross;
-        __syncthreads();
-        if (first) carry = (part[1][0] + part[1][1]) + (part[1][2] + part[1][3]);
-        first = false;
-        double before = carry + s - sum;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            before += k < wave ? part[0][k] : 0.0;
-            carry += part[0][k];
-        }
-#pragma unroll
-        for (int n = 0; n < N; ++n) {
-            const int t = hi - 1 - tid * N - n;
-            if (t >= t0) w.dg[(tok0 + t) * w.HK + hk] = gate[n] < -104.f ? 0.f : (float)(before + v[n]);
-        }
+    for (int n = 0; n < N; ++n) {
+        sum += v[n];
+        v[n] = sum;
     }
+    double s = sum;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        const double u = __shfl_up(s, o, 64);
+        if (lane >= o) s += u;
+        cross += __shfl_xor(cross, o, 64);
+    }
+    if (lane == 63) part[0][wave] = s;
+    if (lane == 0) part[1][wave] = cross;
+    __syncthreads();
+    double before = (part[1][0] + part[1][1]) + (part[1][2] + part[1][3]) + (s - sum);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) before += k < wave ? part[0][k] : 0.0;
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        const int t = live - 1 - tid * N - n;
+        if (t >= t0) w.dg[(tok0 + t) * w.HK + hk] = gate[n] < -104.f ? 0.f : (float)(before + v[n]);
+    }
+    for (int t = live + tid; t < t1; t += THREADS) w.dg[(tok0 + t) * w.HK + hk] = 0.f;
 }
 
 // ---------------------------------------------------------------- one token

@@ -928,7 +928,7 @@ struct GatedPlan {
     size_t fst, rst, dec, rq, rk, total;
 };
 GatedPlan gated_plan(const Seq& s, bool backward) {
-    constexpr int64_t CUS = 256, MOST = 16;
+    constexpr int64_t CUS = 256, MOST = mhla::GATED_MAX_CHUNKS;
     const int64_t C = mhla::GATED_CHUNK, chunks = s.T > 0 ? (s.T + C - 1) / C : 1;
     const int64_t walks = s.B * s.HK * mhla::gated_value_blocks((int)s.D);
     int64_t n = CUS * mhla::gated_walks_per_cu(s.esz == 2, (int)s.D, backward) / walks;
