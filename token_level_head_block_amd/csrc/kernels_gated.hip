@@ -139,22 +139,8 @@ struct Tile {
         }
         return f;
     }
-    // the same in token order
-    __device__ static __forceinline__ Frag<E> rows_t(const char* t, int row0, int kk, int lane) {
-        const int row = row0 + (lane & 15), g = lane >> 4;
-        Frag<E> f;
-        if constexpr (sizeof(E) == 2) {
-            const int half = (g & 1) * 8;
-            const u32x2 a = *reinterpret_cast<const u32x2*>(t + at(row, 4 * kk + (g >> 1)) + half);
-            const u32x2 b = *reinterpret_cast<const u32x2*>(t + at(row, 4 * kk + 2 + (g >> 1)) + half);
-            f.v = u32x4{a[0], a[1], b[0], b[1]};
-        } else {
-            f.a = *reinterpret_cast<const f32x4*>(t + at(row, 8 * kk + g));
-            f.b = *reinterpret_cast<const f32x4*>(t + at(row, 8 * kk + 4 + g));
-        }
-        return f;
-    }
-    // columns 16 n .. 16 n + 15, contraction over rows 32 kk .. 32 kk + 31, token order
+    // columns 16 n .. 16 n + 15, contraction over rows 32 kk .. 32 kk + 31, token order (ROW: row order)
+    template <bool ROW = false>
     __device__ static __forceinline__ Frag<E> cols(const char* t, int kk, int n, int lane) {
         const int i = lane & 15, g = lane >> 4;
         Frag<E> f;
@@ -163,18 +149,18 @@ struct Tile {
             // lane i gets column i of the group's 4 rows
             typedef short s16x4 __attribute__((ext_vector_type(4)));
             typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
-            const int row = 32 * kk + 4 * g + (i >> 2), piece = 2 * n + ((i & 3) >> 1), half = (i & 1) * 8;
+            const int row = 32 * kk + (ROW ? 8 : 4) * g + (i >> 2), piece = 2 * n + ((i & 3) >> 1), half = (i & 1) * 8;
             const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(t + at(row, piece) + half));
-            const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(t + at(row + 16, piece) + half));
+            const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(t + at(row + (ROW ? 4 : 16), piece) + half));
             const u32x2 ua = __builtin_bit_cast(u32x2, a), ub = __builtin_bit_cast(u32x2, b);
             f.v = u32x4{ua[0], ua[1], ub[0], ub[1]};
         } else {
             const int c = 16 * n + i;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const int row = 32 * kk + 4 * g + j;
+                const int row = 32 * kk + (ROW ? 8 : 4) * g + j, row2 = row + (ROW ? 4 : 16);
                 f.a[j] = *reinterpret_cast<const float*>(t + at(row, c >> 2) + (c & 3) * 4);
-                f.b[j] = *reinterpret_cast<const float*>(t + at(row + 16, c >> 2) + (c & 3) * 4);
+                f.b[j] = *reinterpret_cast<const float*>(t + at(row2, c >> 2) + (c & 3) * 4);
             }
         }
         return f;
@@ -486,8 +472,13 @@ __device__ __forceinline__ int xcd_run(int blk, int n) {
 // Pair weights: inside the wave's own 16 tokens each from its two gate sums; with an earlier
 // (later) group of 16 as 2^(G_t - G_b) 2^(G_b - G_s) over the sum at the group's end (before
 // its start), one exponential a row and one a token instead of one a pair.
+template <typename E, int D, int EB, bool DOT>
+constexpr int walk_lds() {
+    return (GC * D + GC * EB + (sizeof(E) == 4 ? 1 : DOT ? 3 : 2) * EB * D) * (int)sizeof(E) + GATE_ROWS * GC * 4;
+}
+
 template <typename E, int D, int EB, bool REV, bool DOT>
-__global__ void __launch_bounds__(THREADS, sizeof(E) == 2 || D <= 64 ? 2 : 1) gated_walk(Walk w) {
+__device__ __forceinline__ void walk(const Walk& w, int id, char* lds) {
     using TY = Tile<E, D>;
     using TZ = Tile<E, EB>;
     using ST = StateTiles<D, EB>;
@@ -495,7 +486,6 @@ __global__ void __launch_bounds__(THREADS, sizeof(E) == 2 || D <= 64 ? 2 : 1) ga
     constexpr int NP = sizeof(E) == 4 ? 1 : 2;             // terms of P
     constexpr int KD = D / 32, KE = EB / 32, ET = EB / 16;
     constexpr int YB = GC * TY::ROWB, ZB = GC * TZ::ROWB, SB = EB * TY::ROWB;
-    __shared__ __attribute__((aligned(16))) char lds[YB + ZB + NS * SB + GATE_ROWS * GC * 4];
     char* yt = lds;
     char* zt = lds + YB;
     char* stt = lds + YB + ZB;   // S transposed, [e][c], NS terms
@@ -507,7 +497,6 @@ __global__ void __launch_bounds__(THREADS, sizeof(E) == 2 || D <= 64 ? 2 : 1) ga
     const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, li = lane & 15,
               lg = lane >> 4;
     constexpr int NB = D / EB;
-    int id = xcd_run(blockIdx.x, gridDim.x);
     const int eb = id % NB;
     id /= NB;
     const int hk = id % w.HK;
@@ -559,8 +548,9 @@ __global__ void __launch_bounds__(THREADS, sizeof(E) == 2 || D <= 64 ? 2 : 1) ga
         zs.load(rows_of<E>(w.z.p, tk, w.z.stride, h * D + eb * EB, live, EB), (int)w.z.stride, tid);
         graw = __int_as_float(__builtin_amdgcn_raw_buffer_load_b32(rows_of<float>(w.g, tk, w.HK, hk, live, 1), lane * w.HK * 4, 0, 0));
     };
-    Frag<E> xf[KD], x2f[DOT ? KE : 1];
-    auto fetch_x = [&](int ci, int hx, Frag<E> (&x)[KD], Frag<E> (&x2)[DOT ? KE : 1]) {
+    // x2 in row order for its product with Z, and in token order, as the accumulators hold the output
+    Frag<E> xf[KD], x2f[DOT ? KE : 1], x2t[DOT ? KE : 1];
+    auto fetch_x = [&](int ci, int hx, Frag<E> (&x)[KD], Frag<E> (&x2)[DOT ? KE : 1], Frag<E> (&xt)[DOT ? KE : 1]) {
         const int c = first + dir * ci;
         const int live = ci < chunks ? min(len - c * GC, GC) : 0;
         const int64_t tk = tok0 + (int64_t)c * GC;
@@ -571,11 +561,14 @@ __global__ void __launch_bounds__(THREADS, sizeof(E) == 2 || D <= 64 ? 2 : 1) ga
         if constexpr (DOT) {
             const __amdgpu_buffer_rsrc_t r2 = rows_of<E>(w.x2.p, tk, w.x2.stride, h * D + eb * EB, live, EB);
 #pragma unroll
-            for (int kk = 0; kk < KE; ++kk) load_row_t(r2, (tl * (int)w.x2.stride + 4 * lg + 32 * kk) * ES, x2[kk]);
+            for (int kk = 0; kk < KE; ++kk) {
+                load_row(r2, (tl * (int)w.x2.stride + 8 * lg + 32 * kk) * ES, x2[kk]);
+                load_row_t(r2, (tl * (int)w.x2.stride + 4 * lg + 32 * kk) * ES, xt[kk]);
+            }
         }
     };
     fetch(0, 0);
-    fetch_x(0, 0, xf, x2f);
+    fetch_x(0, 0, xf, x2f, x2t);
 
     const bool keep = w.end && (REV ? seg == 0 : seg == w.nseg - 1);   // the state after the last chunk is wanted
     f32x4 o[ET];
@@ -608,8 +601,8 @@ __global__ void __launch_bounds__(THREADS, sizeof(E) == 2 || D <= 64 ? 2 : 1) ga
             for (int hx = 0; hx < nx; ++hx) {
                 const bool last_x = hx + 1 == nx;
                 asm volatile("" ::: "memory");    // reads of the tiles stay in the loop: hoisted, they fill the registers
-                Frag<E> xn[KD], x2n[DOT ? KE : 1];
-                if (!REV || last_y) fetch_x(last_x ? ci + 1 : ci, last_x ? 0 : hx + 1, xn, x2n);
+                Frag<E> xn[KD], x2n[DOT ? KE : 1], xtn[DOT ? KE : 1];
+                if (!REV || last_y) fetch_x(last_x ? ci + 1 : ci, last_x ? 0 : hx + 1, xn, x2n, xtn);
                 if (!REV || hy == 0) {
                     // from the state: o = S^T x
                     rsum = 0.f;
@@ -627,7 +620,7 @@ __global__ void __launch_bounds__(THREADS, sizeof(E) == 2 || D <= 64 ? 2 : 1) ga
 #pragma unroll
                         for (int kk = 0; kk < KE; ++kk) {
                             float u[8];
-                            widen(x2f[kk], u);
+                            widen(x2t[kk], u);
 #pragma unroll
                             for (int j = 0; j < 4; ++j) rsum += u[j] * o[2 * kk][j] + u[4 + j] * o[2 * kk + 1][j];
                         }
@@ -648,7 +641,7 @@ __global__ void __launch_bounds__(THREADS, sizeof(E) == 2 || D <= 64 ? 2 : 1) ga
                     for (int k = 0; k < KD; ++k) acc = mma(TY::rows(yt, 16 * st, k, lane), xf[k], acc);
                     if constexpr (DOT) {
 #pragma unroll
-                        for (int k = 0; k < KE; ++k) m = mma(TZ::rows_t(zt, 16 * st, k, lane), x2f[k], m);
+                        for (int k = 0; k < KE; ++k) m = mma(TZ::rows(zt, 16 * st, k, lane), x2f[k], m);
                     }
                     const float rf = group_factor<REV>(gh, th, tf, st, wave);
                     const f32x4 cs = *reinterpret_cast<const f32x4*>(cw + 16 * st + 4 * lg);
@@ -664,7 +657,7 @@ __global__ void __launch_bounds__(THREADS, sizeof(E) == 2 || D <= 64 ? 2 : 1) ga
                     for (int k = 0; k < KD; ++k) acc = mma(TY::rows(yt, 16 * wave, k, lane), xf[k], acc);
                     if constexpr (DOT) {
 #pragma unroll
-                        for (int k = 0; k < KE; ++k) m = mma(TZ::rows_t(zt, 16 * wave, k, lane), x2f[k], m);
+                        for (int k = 0; k < KE; ++k) m = mma(TZ::rows(zt, 16 * wave, k, lane), x2f[k], m);
                     }
                     const f32x4 ow = own_weights<REV>(gh, th, tf, w.pair_scale, wave, lane);
 #pragma unroll
@@ -715,7 +708,10 @@ __global__ void __launch_bounds__(THREADS, sizeof(E) == 2 || D <= 64 ? 2 : 1) ga
                     for (int kk = 0; kk < KD; ++kk) xf[kk] = xn[kk];
                     if constexpr (DOT) {
 #pragma unroll
-                        for (int kk = 0; kk < KE; ++kk) x2f[kk] = x2n[kk];
+                        for (int kk = 0; kk < KE; ++kk) {
+                            x2f[kk] = x2n[kk];
+                            x2t[kk] = xtn[kk];
+                        }
                     }
                 }
             }
@@ -727,12 +723,17 @@ __global__ void __launch_bounds__(THREADS, sizeof(E) == 2 || D <= 64 ? 2 : 1) ga
         store_state<D, EB>(S, w.end + ((int64_t)b * w.HK + hk) * D * D + eb * EB * w.se, w.sc, w.se, wave, lane);
 }
 
+template <typename E, int D, int EB>
+__global__ void __launch_bounds__(THREADS, sizeof(E) == 2 || D <= 64 ? 2 : 1) gated_walk(Walk w) {
+    __shared__ __attribute__((aligned(16))) char lds[walk_lds<E, D, EB, false>()];
+    walk<E, D, EB, false, false>(w, xcd_run(blockIdx.x, gridDim.x), lds);
+}
+
 // ---------------------------------------------------------------- dk and dv together
 // Backwards over a segment with X = k and v, Y = q, Z = do: the pair products q . k and
 // do . v serve dk, dv and k . dk alike, the tiles are read once and the state's gradient D is
 // summed once, where two walks would do each twice.  D lies in LDS once, transposed ([e][c]):
-// dv contracts it over c (its columns), dk over e (its rows, by transposing reads), so k and
-// v are held in token order.  D <= 64: at 128 the state of all columns leaves room for one
+// dv contracts it over c (its columns), dk over e (its rows, by transposing reads).  D <= 64: at 128 the state of all columns leaves room for one
 // workgroup of a compute unit, and dk and dv are walks of their own.
 struct Back {
     Role q, k, v, dout;
@@ -748,7 +749,7 @@ struct Back {
 };
 
 template <typename E, int D>
-__global__ void __launch_bounds__(THREADS, sizeof(E) == 2 || D == 32 ? 2 : 1) gated_back(Back w) {
+__device__ __forceinline__ void back(const Back& w, int id, char* lds) {
     using TL = Tile<E, D>;
     using ST = StateTiles<D, D>;
     constexpr int NS = sizeof(E) == 4 ? 1 : 3;             // terms of D (two for dv, three for k . dk)
@@ -756,7 +757,6 @@ __global__ void __launch_bounds__(THREADS, sizeof(E) == 2 || D == 32 ? 2 : 1) ga
     constexpr int NP = sizeof(E) == 4 ? 1 : 2;
     constexpr int KD = D / 32, DT = D / 16, ES = (int)sizeof(E);
     constexpr int TB = GC * TL::ROWB, SB = D * TL::ROWB;
-    __shared__ __attribute__((aligned(16))) char lds[2 * TB + NS * SB + GATE_ROWS * GC * 4];
     char* yt = lds;
     char* zt = lds + TB;
     char* stt = lds + 2 * TB;
@@ -767,7 +767,6 @@ __global__ void __launch_bounds__(THREADS, sizeof(E) == 2 || D == 32 ? 2 : 1) ga
 
     const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, li = lane & 15,
               lg = lane >> 4;
-    int id = xcd_run(blockIdx.x, gridDim.x);
     const int hk = id % w.HK;
     id /= w.HK;
     const int seg = id % w.nseg, b = id / w.nseg;
@@ -806,8 +805,9 @@ __global__ void __launch_bounds__(THREADS, sizeof(E) == 2 || D == 32 ? 2 : 1) ga
         zs.load(rows_of<E>(w.dout.p, tk, w.dout.stride, h * D, live, D), (int)w.dout.stride, tid);
         graw = __int_as_float(__builtin_amdgcn_raw_buffer_load_b32(rows_of<float>(w.g, tk, w.HK, hk, live, 1), lane * w.HK * 4, 0, 0));
     };
-    Frag<E> kf[KD], vf[KD], kn[KD], vn[KD];
-    auto fetch_x = [&](int ci, Frag<E> (&k)[KD], Frag<E> (&v)[KD]) {
+    // k also in token order, as the accumulators hold dk
+    Frag<E> kf[KD], kt[KD], vf[KD], kn[KD], ktn[KD], vn[KD];
+    auto fetch_x = [&](int ci, Frag<E> (&k)[KD], Frag<E> (&kt)[KD], Frag<E> (&v)[KD]) {
         const int c = live_end - 1 - ci;
         const int live = ci < chunks ? min(len - c * GC, GC) : 0;
         const int64_t tk = tok0 + (int64_t)c * GC;
@@ -815,12 +815,13 @@ __global__ void __launch_bounds__(THREADS, sizeof(E) == 2 || D == 32 ? 2 : 1) ga
         const __amdgpu_buffer_rsrc_t rv = rows_of<E>(w.v.p, tk, w.v.stride, hk * D, live, D);
 #pragma unroll
         for (int kk = 0; kk < KD; ++kk) {
-            load_row_t(rk, (tl * (int)w.k.stride + 4 * lg + 32 * kk) * ES, k[kk]);
-            load_row_t(rv, (tl * (int)w.v.stride + 4 * lg + 32 * kk) * ES, v[kk]);
+            load_row(rk, (tl * (int)w.k.stride + 8 * lg + 32 * kk) * ES, k[kk]);
+            load_row_t(rk, (tl * (int)w.k.stride + 4 * lg + 32 * kk) * ES, kt[kk]);
+            load_row(rv, (tl * (int)w.v.stride + 8 * lg + 32 * kk) * ES, v[kk]);
         }
     };
     fetch(0, 0);
-    fetch_x(0, kf, vf);
+    fetch_x(0, kf, kt, vf);
 
     const bool keep = w.end && seg == 0;
     f32x4 ok[DT], ov[DT];
@@ -849,7 +850,7 @@ __global__ void __launch_bounds__(THREADS, sizeof(E) == 2 || D == 32 ? 2 : 1) ga
             const bool last = hy + 1 == w.G;
             fetch(last ? ci + 1 : ci, last ? 0 : hy + 1);
             if (hy == 0) {
-                fetch_x(ci + 1, kn, vn);
+                fetch_x(ci + 1, kn, ktn, vn);
                 // from the state: dv = D^T k, dk = D v
                 const float trw = rw[tl];
                 rsum = 0.f;
@@ -860,8 +861,8 @@ __global__ void __launch_bounds__(THREADS, sizeof(E) == 2 || D == 32 ? 2 : 1) ga
                     for (int n = NS - 1; n >= 0; --n)
 #pragma unroll
                         for (int kk = 0; kk < KD; ++kk) {
-                            if (n < NSV) a = mma(TL::rows_t(stt + n * SB, 16 * e, kk, lane), kf[kk], a);
-                            c2 = mma(TL::cols(stt + n * SB, kk, e, lane), vf[kk], c2);
+                            if (n < NSV) a = mma(TL::rows(stt + n * SB, 16 * e, kk, lane), kf[kk], a);
+                            c2 = mma(TL::template cols<true>(stt + n * SB, kk, e, lane), vf[kk], c2);
                         }
                     ov[e] = a * trw;
                     ok[e] = c2 * trw;
@@ -869,7 +870,7 @@ __global__ void __launch_bounds__(THREADS, sizeof(E) == 2 || D == 32 ? 2 : 1) ga
 #pragma unroll
                 for (int kk = 0; kk < KD; ++kk) {
                     float u[8];
-                    widen(kf[kk], u);
+                    widen(kt[kk], u);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) rsum += u[j] * ok[2 * kk][j] + u[4 + j] * ok[2 * kk + 1][j];
                 }
@@ -883,8 +884,8 @@ __global__ void __launch_bounds__(THREADS, sizeof(E) == 2 || D == 32 ? 2 : 1) ga
                 f32x4 a = {0.f, 0.f, 0.f, 0.f}, c2 = a;
 #pragma unroll
                 for (int k = 0; k < KD; ++k) {
-                    a = mma(TL::rows_t(yt, 16 * st, k, lane), kf[k], a);
-                    c2 = mma(TL::rows_t(zt, 16 * st, k, lane), vf[k], c2);
+                    a = mma(TL::rows(yt, 16 * st, k, lane), kf[k], a);
+                    c2 = mma(TL::rows(zt, 16 * st, k, lane), vf[k], c2);
                 }
                 const float rf = group_factor<true>(gh, th, tf, st, wave);
                 const f32x4 cs = *reinterpret_cast<const f32x4*>(cw + 16 * st + 4 * lg);
@@ -900,8 +901,8 @@ __global__ void __launch_bounds__(THREADS, sizeof(E) == 2 || D == 32 ? 2 : 1) ga
                 f32x4 a = {0.f, 0.f, 0.f, 0.f}, c2 = a;
 #pragma unroll
                 for (int k = 0; k < KD; ++k) {
-                    a = mma(TL::rows_t(yt, 16 * wave, k, lane), kf[k], a);
-                    c2 = mma(TL::rows_t(zt, 16 * wave, k, lane), vf[k], c2);
+                    a = mma(TL::rows(yt, 16 * wave, k, lane), kf[k], a);
+                    c2 = mma(TL::rows(zt, 16 * wave, k, lane), vf[k], c2);
                 }
                 const f32x4 ow = own_weights<true>(gh, th, tf, w.scale, wave, lane);
 #pragma unroll
@@ -964,10 +965,36 @@ __global__ void __launch_bounds__(THREADS, sizeof(E) == 2 || D == 32 ? 2 : 1) ga
 #pragma unroll
         for (int kk = 0; kk < KD; ++kk) {
             kf[kk] = kn[kk];
+            kt[kk] = ktn[kk];
             vf[kk] = vn[kk];
         }
     }
     if (keep) store_state<D, D>(S, w.end + pair * D * D, D, 1, wave, lane);
+}
+
+// All three gradients in one launch: the walks for dq and for dk and dv (at D = 128 for dv
+// and for dk) do not wait for each other, short problems run them side by side and long ones
+// fill the last round.  The walks of one segment have neighbouring numbers, the longest first.
+struct Grads {
+    Walk q, v, k;   // D = 128: v and k
+    Back kv;        // D <= 64
+};
+template <typename E, int D, int EB>
+__global__ void __launch_bounds__(THREADS, sizeof(E) == 2 || D == 32 ? 2 : 1) gated_grads(Grads w) {
+    constexpr int NB = D / EB;
+    constexpr int LDS = walk_lds<E, D, EB, true>();   // of D <= 64 the same for back()
+    __shared__ __attribute__((aligned(16))) char lds[LDS];
+    const int n = xcd_run(blockIdx.x, gridDim.x);
+    if constexpr (NB == 1) {
+        static_assert(D == EB, "back() has all columns");
+        if ((n & 1) == 0) back<E, D>(w.kv, n >> 1, lds);
+        else walk<E, D, EB, false, true>(w.q, n >> 1, lds);
+    } else {
+        const int role = (n / NB) % 3, id = n / (3 * NB) * NB + n % NB;
+        if (role == 0) walk<E, D, EB, true, true>(w.k, id, lds);
+        else if (role == 1) walk<E, D, EB, false, true>(w.q, id, lds);
+        else walk<E, D, EB, true, false>(w.v, id, lds);
+    }
 }
 
 // ---------------------------------------------------------------- segments
@@ -1307,14 +1334,6 @@ __global__ void __launch_bounds__(THREADS) gated_step(GatedStep w) {
 }
 
 // ---------------------------------------------------------------- launches
-template <typename E, int D, bool REV, bool DOT>
-hipError_t launch_walk(const Walk& w, hipStream_t stream) {
-    constexpr int EB = D < 64 ? D : 64;
-    const int64_t n = (int64_t)w.B * w.HK * w.nseg * (D / EB);
-    gated_walk<E, D, EB, REV, DOT><<<dim3((unsigned)n), THREADS, 0, stream>>>(w);
-    return hipGetLastError();
-}
-
 template <typename E, int D>
 hipError_t launch_local(const Local& w, hipStream_t stream) {
     constexpr int EB = D < 64 ? D : 64;
@@ -1374,7 +1393,9 @@ hipError_t forward(const GatedForward& f) {
     w.B = p.B; w.T = p.T; w.HK = p.HK; w.nx = p.H / p.HK; w.ny = 1; w.nseg = p.nseg; w.seg_chunks = p.seg_chunks;
     w.pair_scale = w.row_scale = p.scale;
     w.key_scale = 1.f;
-    return launch_walk<E, D, false, false>(w, p.stream);
+    constexpr int EB = D < 64 ? D : 64;
+    gated_walk<E, D, EB><<<dim3((unsigned)((int64_t)p.B * p.HK * p.nseg * (D / EB))), THREADS, 0, p.stream>>>(w);
+    return hipGetLastError();
 }
 
 template <typename E, int D>
@@ -1405,12 +1426,12 @@ hipError_t backward(const GatedBackward& f) {
     if ((err = launch_local<E, D>(l, p.stream)) != hipSuccess) return err;
     if ((err = launch_join(f.fst, p.s0, f.rst, f.ds1, f.fdec, p.B * p.HK, p.nseg, DD, p.stream)) != hipSuccess) return err;
 
-    Walk w = {};
+    Grads gr = {};
+    Walk& w = gr.q;       // dq and q . dq
     w.g = p.g;
     w.lens = p.lens;
     w.B = p.B; w.T = p.T; w.HK = p.HK; w.nseg = p.nseg; w.seg_chunks = p.seg_chunks;
     w.start_seg = DD;
-    // dq and q . dq
     w.x = {f.dout, hs};
     w.y = {p.v, p.vs};
     w.z = {p.k, p.ks};
@@ -1423,9 +1444,8 @@ hipError_t backward(const GatedBackward& f) {
     w.nx = G; w.ny = 1;
     w.pair_scale = w.row_scale = p.scale;
     w.key_scale = 1.f;
-    if ((err = launch_walk<E, D, false, true>(w, p.stream)) != hipSuccess) return err;
     if constexpr (D <= 64) {
-        Back k = {};
+        Back& k = gr.kv;
         k.q = {p.q, p.qs};
         k.k = {p.k, p.ks};
         k.v = {p.v, p.vs};
@@ -1439,35 +1459,37 @@ hipError_t backward(const GatedBackward& f) {
         k.end = f.ds0;
         k.B = p.B; k.T = p.T; k.HK = p.HK; k.G = G; k.nseg = p.nseg; k.seg_chunks = p.seg_chunks;
         k.scale = p.scale;
-        gated_back<E, D><<<dim3((unsigned)((int64_t)p.B * p.HK * p.nseg)), THREADS, 0, p.stream>>>(k);
-        if ((err = hipGetLastError()) != hipSuccess) return err;
     } else {
-        // dv, and the initial state's gradient
-        w.x = {p.k, p.ks};
-        w.y = {p.q, p.qs};
-        w.z = {f.dout, hs};
-        w.x2 = {nullptr, 0};
-        w.out = f.dv;
-        w.r = nullptr;
-        w.start = f.rst;
-        w.start_pair = (int64_t)p.nseg * DD;
-        w.end = f.ds0;
-        w.sc = D; w.se = 1;
-        w.nx = 1; w.ny = G;
-        w.row_scale = 1.f;
-        w.key_scale = p.scale;
-        if ((err = launch_walk<E, D, true, false>(w, p.stream)) != hipSuccess) return err;
-        // dk and k . dk
-        w.x = {p.v, p.vs};
-        w.y = {f.dout, hs};
-        w.z = {p.q, p.qs};
-        w.x2 = {p.k, p.ks};
-        w.out = f.dk;
-        w.r = f.rk;
-        w.end = nullptr;
-        w.sc = 1; w.se = D;
-        if ((err = launch_walk<E, D, true, true>(w, p.stream)) != hipSuccess) return err;
+        Walk& v = gr.v;   // dv, and the initial state's gradient
+        v = w;
+        v.x = {p.k, p.ks};
+        v.y = {p.q, p.qs};
+        v.z = {f.dout, hs};
+        v.x2 = {nullptr, 0};
+        v.out = f.dv;
+        v.r = nullptr;
+        v.start = f.rst;
+        v.start_pair = (int64_t)p.nseg * DD;
+        v.end = f.ds0;
+        v.sc = D; v.se = 1;
+        v.nx = 1; v.ny = G;
+        v.row_scale = 1.f;
+        v.key_scale = p.scale;
+        Walk& k = gr.k;   // dk and k . dk
+        k = v;
+        k.x = {p.v, p.vs};
+        k.y = {f.dout, hs};
+        k.z = {p.q, p.qs};
+        k.x2 = {p.k, p.ks};
+        k.out = f.dk;
+        k.r = f.rk;
+        k.end = nullptr;
+        k.sc = 1; k.se = D;
     }
+    constexpr int EB = D < 64 ? D : 64;
+    gated_grads<E, D, EB><<<dim3((unsigned)((int64_t)p.B * p.HK * p.nseg * (D / EB) * (D <= 64 ? 2 : 3))), THREADS, 0,
+                            p.stream>>>(gr);
+    if ((err = hipGetLastError()) != hipSuccess) return err;
 
     GateGrad d;
     d.rq = f.rq; d.rk = f.rk; d.fst = f.fst; d.rst = f.rst; d.g = p.g; d.lens = p.lens; d.dg = f.dg;

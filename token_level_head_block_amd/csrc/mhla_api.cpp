@@ -958,10 +958,10 @@ mhla_status check_gated(const mhla_seq* seq, Seq* s) {
     const mhla_status st = check_seq(seq, s, true);
     if (st != MHLA_OK) return st;
     if (s->empty()) return MHLA_OK;
-    // workgroups of a launch: two roles of a segment's value blocks at most
+    // workgroups of a launch: three walks of a segment's value blocks at most
     const double walks = (double)s->B * (double)s->HK * mhla::gated_value_blocks((int)s->D);
     const double segs = (double)s->T / mhla::GATED_CHUNK + 1;
-    if (walks >= 1073741824.0 || walks * segs * 2 >= 2147483648.0) return MHLA_ERR_UNSUPPORTED;
+    if (walks >= 1073741824.0 || walks * segs * 3 >= 2147483648.0) return MHLA_ERR_UNSUPPORTED;
     return MHLA_OK;
 }
 
