@@ -100,9 +100,12 @@ def test_workspace_holds_segment_states():
     up = lambda x: (x + 255) // 256 * 256  # noqa: E731
     many = mh.make_seq(64, 4096, 16, 16, 64, mh.MHLA_BF16)
     assert mh.mhla_gated_workspace_bytes(many) == 0              # enough heads: a sequence is one segment
-    few = mh.make_seq(1, 64 * 8, 1, 1, 64, mh.MHLA_BF16)         # a segment a chunk
-    assert mh.mhla_gated_workspace_bytes(few) == up(9 * 64 * 64 * 4) + up(8 * 4)
-    n = up(9 * 64 * 64 * 4) + up(8 * 4) + up(8 * 64 * 64 * 4) + 2 * up(512 * 4)
+    short = mh.make_seq(1, 256, 1, 1, 64, mh.MHLA_BF16)          # few chunks: one segment as well
+    assert mh.mhla_gated_workspace_bytes(short) == 0
+    assert mh.mhla_gated_backward_workspace_bytes(short) == up(64 * 64 * 4) + 2 * up(256 * 4)
+    few = mh.make_seq(1, 64 * 9, 1, 1, 64, mh.MHLA_BF16)         # a segment a chunk
+    assert mh.mhla_gated_workspace_bytes(few) == up(10 * 64 * 64 * 4) + up(9 * 4)
+    n = up(10 * 64 * 64 * 4) + up(9 * 4) + up(9 * 64 * 64 * 4) + 2 * up(576 * 4)
     assert mh.mhla_gated_backward_workspace_bytes(few) == n
 
 

@@ -518,7 +518,7 @@ def _call(fn, device, stream, *args) -> int:
     """fn(*args, stream) with `device` current; stream: None for its current one."""
     import torch
     if stream is None:
-        s = torch.cuda.current_stream(device).cuda_stream
+        s = torch._C._cuda_getCurrentRawStream(device.index)     # current_stream() without its object
     else:
         s = stream if isinstance(stream, int) else stream.cuda_stream
     if device.index == torch.cuda.current_device():

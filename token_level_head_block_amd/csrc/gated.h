@@ -29,9 +29,10 @@ struct GatedProblem {
     hipStream_t stream;
 };
 
-// Workspace regions of a split sequence: for every (b, kv head) nseg + 1 (before
-// each segment, and after the last) or nseg (after each segment) states of D x D
-// fp32 and nseg segment decays.
+// Workspace regions of a split sequence (nseg > 1): for every (b, kv head) nseg + 1
+// (before each segment, and after the last) or nseg (after each segment) states of D x D
+// fp32 and nseg segment decays.  Backwards with one segment fst holds the state after the
+// sequence alone (where the final state's gradient is given).
 struct GatedForward {
     GatedProblem p;
     void* out;
@@ -59,16 +60,18 @@ struct GatedBackward {
 hipError_t run_gated_backward(const GatedBackward& f);
 
 // Value columns that one workgroup of the walk holds, and their blocks.
-inline int gated_value_block(int D) { return D < 64 ? D : 64; }
+constexpr int gated_value_block(int D) { return D < 64 ? D : 64; }
 inline int gated_value_blocks(int D) { return D / gated_value_block(D); }
 
-// Walks (workgroups) that a compute unit holds side by side, by their registers and LDS:
-// bf16 forwards 150 registers and 34 KB at head_dim 64 (three), 212 and 59 KB at 128 (two);
-// backwards 234 and 43 KB (two).  fp32 operands take twice the room.
+// Walks (workgroups) of a split sequence for each compute unit, about as many as it holds by
+// registers and LDS.  Measured with 1, 2 and 3: forwards one sequence of 65536 tokens, 6 heads
+// of 64 bf16: 96, 80, 82 us; 2 x 4096 tokens, 70 heads of 32 fp32: 171, 138, 122 us; backwards
+// 2 x 4097 tokens, 12 heads over 4 of 128: 182, 168, 176 us; 4 x 4096, 8 heads of 64 fp32:
+// 219, 228, 257 us.
 inline int gated_walks_per_cu(bool bf16, int D, bool backward) {
     if (D == 128) return bf16 ? 2 : 1;
     if (backward) return bf16 || D == 32 ? 2 : 1;
-    return bf16 || D == 32 ? 3 : 2;
+    return D == 32 ? 3 : 2;
 }
 
 struct GatedStep {

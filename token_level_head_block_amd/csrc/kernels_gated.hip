@@ -21,7 +21,7 @@ namespace mhla {
 namespace {
 
 constexpr int GC = GATED_CHUNK;
-constexpr int THREADS = 256;
+constexpr int THREADS = 256;   // a group of four waves
 constexpr float LOG2E = 1.44269504088896341f;
 constexpr float LOG2E_LOW = 1.92596299e-8f;    // log2(e) - LOG2E
 
@@ -30,6 +30,9 @@ constexpr float LOG2E_LOW = 1.92596299e-8f;    // log2(e) - LOG2E
 // holds row i's values in one of two orders, the same for both operands of a product:
 // "row" order, 8g + j (j < 8), or "token" order, 16 (j / 4) + 4g + j % 4, in which a
 // pair of accumulator tiles (rows 4g + 0..3 of column i) is an operand as it stands.
+// Where a product's rows are value columns, two tiles take them interleaved: row 4g + j of
+// tiles 2k and 2k + 1 is column 32k + 8g + j and 32k + 8g + 4 + j, so that a lane ends up with
+// the eight neighbouring columns that it has of an operand in row order.
 // bf16: one 16x16x32 product; fp32: eight 16x16x4 products.
 template <typename E>
 struct Frag;
@@ -139,33 +142,38 @@ struct Tile {
         }
         return f;
     }
-    // columns 16 n .. 16 n + 15, contraction over rows 32 kk .. 32 kk + 31, token order (ROW: row order)
-    template <bool ROW = false>
+    // columns of tile n (INTER: interleaved with its neighbour's), contraction over rows
+    // 32 kk .. 32 kk + 31, token order
+    template <bool INTER>
     __device__ static __forceinline__ Frag<E> cols(const char* t, int kk, int n, int lane) {
         const int i = lane & 15, g = lane >> 4;
         Frag<E> f;
         if constexpr (sizeof(E) == 2) {
-            // transposing reads: in a group of 16 lanes, 4 lanes address the 32 bytes of one row,
-            // lane i gets column i of the group's 4 rows
+            // transposing reads: in a group of 16 lanes, 4 lanes address 8 bytes each of one row, lane i gets
+            // the i-th of these columns of the group's 4 rows
             typedef short s16x4 __attribute__((ext_vector_type(4)));
             typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
-            const int row = 32 * kk + (ROW ? 8 : 4) * g + (i >> 2), piece = 2 * n + ((i & 3) >> 1), half = (i & 1) * 8;
+            const int row = 32 * kk + 4 * g + (i >> 2);
+            const int piece = INTER ? 4 * (n >> 1) + (i & 3) : 2 * n + ((i & 3) >> 1), half = (INTER ? n & 1 : i & 1) * 8;
             const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(t + at(row, piece) + half));
-            const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(t + at(row + (ROW ? 4 : 16), piece) + half));
+            const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(t + at(row + 16, piece) + half));
             const u32x2 ua = __builtin_bit_cast(u32x2, a), ub = __builtin_bit_cast(u32x2, b);
             f.v = u32x4{ua[0], ua[1], ub[0], ub[1]};
         } else {
-            const int c = 16 * n + i;
+            const int c = INTER ? 32 * (n >> 1) + 8 * (i >> 2) + 4 * (n & 1) + (i & 3) : 16 * n + i;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const int row = 32 * kk + (ROW ? 8 : 4) * g + j, row2 = row + (ROW ? 4 : 16);
+                const int row = 32 * kk + 4 * g + j;
                 f.a[j] = *reinterpret_cast<const float*>(t + at(row, c >> 2) + (c & 3) * 4);
-                f.b[j] = *reinterpret_cast<const float*>(t + at(row2, c >> 2) + (c & 3) * 4);
+                f.b[j] = *reinterpret_cast<const float*>(t + at(row + 16, c >> 2) + (c & 3) * 4);
             }
         }
         return f;
     }
 };
+// The row of S^T in LDS that holds value column e: the 16 rows of a tile, as interleaved
+// tiles take them, lie together.
+__device__ __forceinline__ int state_row(int e) { return (e & ~31) + 16 * ((e >> 2) & 1) + 4 * ((e >> 3) & 3) + (e & 3); }
 
 // Four fp32 values to columns c .. c + 3 (c a multiple of 4) of a row, split over N tiles.
 template <typename E, int W, int N>
@@ -206,10 +214,6 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_of(const void* p, int64_t
 __device__ __forceinline__ u32x4 load16(__amdgpu_buffer_rsrc_t r, int off) {
     return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
 }
-__device__ __forceinline__ u32x2 load8b(__amdgpu_buffer_rsrc_t r, int off) {
-    return __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, 0));
-}
-
 // 16-byte pieces of a chunk's rows (W values) held in registers between their load and
 // their store to LDS.
 template <typename E, int W>
@@ -235,27 +239,20 @@ struct Staged {
     }
 };
 
-// One row's operand: row order (off at value 8 g) or token order (off at value 4 g).
+// One row's operand in row order: off at value 8 g.
 __device__ __forceinline__ void load_row(__amdgpu_buffer_rsrc_t r, int off, Frag<uint16_t>& f) { f.v = load16(r, off); }
 __device__ __forceinline__ void load_row(__amdgpu_buffer_rsrc_t r, int off, Frag<float>& f) {
     f.a = __builtin_bit_cast(f32x4, load16(r, off));
     f.b = __builtin_bit_cast(f32x4, load16(r, off + 16));
 }
-__device__ __forceinline__ void load_row_t(__amdgpu_buffer_rsrc_t r, int off, Frag<uint16_t>& f) {
-    const u32x2 a = load8b(r, off), b = load8b(r, off + 32);
-    f.v = u32x4{a[0], a[1], b[0], b[1]};
+// Eight neighbouring values of a row, from two interleaved tiles.
+__device__ __forceinline__ void store_row8(__amdgpu_buffer_rsrc_t r, int off, const f32x4& x, const f32x4& y, uint16_t) {
+    const u32x4 w = {pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3])};
+    __builtin_amdgcn_raw_buffer_store_b128(w, r, off, 0, 0);
 }
-__device__ __forceinline__ void load_row_t(__amdgpu_buffer_rsrc_t r, int off, Frag<float>& f) {
-    f.a = __builtin_bit_cast(f32x4, load16(r, off));
-    f.b = __builtin_bit_cast(f32x4, load16(r, off + 64));
-}
-// Four neighbouring values of a row.
-__device__ __forceinline__ void store_row4(__amdgpu_buffer_rsrc_t r, int off, const f32x4& x, uint16_t) {
-    const u32x2 w = {pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3])};
-    __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, w), r, off, 0, 0);
-}
-__device__ __forceinline__ void store_row4(__amdgpu_buffer_rsrc_t r, int off, const f32x4& x, float) {
+__device__ __forceinline__ void store_row8(__amdgpu_buffer_rsrc_t r, int off, const f32x4& x, const f32x4& y, float) {
     __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, x), r, off, 0, 0);
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, y), r, off + 16, 0, 0);
 }
 
 __device__ __forceinline__ f32x4 load4(const uint16_t* p) {
@@ -387,7 +384,7 @@ __device__ __forceinline__ void update_state(typename StateTiles<D, EB>::Acc& S,
 #pragma unroll
         for (int a = 0; a < ST::CW; ++a) {
             float x[8];
-            widen(Tile<E, D>::cols(yt, kk, ST::ct(wave, a), lane), x);
+            widen(Tile<E, D>::template cols<false>(yt, kk, ST::ct(wave, a), lane), x);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 x[j] *= w0[j];
@@ -397,7 +394,7 @@ __device__ __forceinline__ void update_state(typename StateTiles<D, EB>::Acc& S,
         }
 #pragma unroll
         for (int b = 0; b < ST::EW; ++b) {
-            const Frag<E> z = Tile<E, EB>::cols(zt, kk, ST::et(wave, b), lane);
+            const Frag<E> z = Tile<E, EB>::template cols<false>(zt, kk, ST::et(wave, b), lane);
 #pragma unroll
             for (int a = 0; a < ST::CW; ++a)
 #pragma unroll
@@ -434,6 +431,16 @@ __device__ __forceinline__ void store_state(const typename StateTiles<D, EB>::Ac
         }
 }
 
+// Keeps reads of the tiles inside the loop over heads and chunks: hoisted out of it, they fill
+// the registers.  FRESH: their addresses too (the lane number comes back as a value that the
+// compiler knows nothing of).
+template <bool FRESH>
+__device__ __forceinline__ int in_loop(int lane) {
+    if constexpr (FRESH) asm volatile("" : "+v"(lane) : : "memory");
+    else asm volatile("" : : : "memory");
+    return lane;
+}
+
 // ---------------------------------------------------------------- the walk
 // One role: [B, T, heads, D] with a token stride.
 struct Role {
@@ -463,10 +470,16 @@ __device__ __forceinline__ int xcd_run(int blk, int n) {
     return x * q + min(x, r) + (blk >> 3);
 }
 
-// A workgroup of four waves walks the chunks of one segment of one (b, kv head), for EB of
-// the value columns.  Wave w has the chunk's tokens 16 w .. 16 w + 15 as rows; products are
-// formed transposed (Y X^T, then Z^T P^T), so that P leaves the accumulators as the next
-// product's operand and a lane stores four neighbouring values of one token.
+// A workgroup walks the chunks of one segment of one (b, kv head), for EB of the value
+// columns, with two groups of four waves side by side: one has the rows (its wave w the
+// chunk's tokens 16 w .. 16 w + 15) and computes the outputs from tiles and state in LDS, the
+// other has the state in its accumulators, adds the chunk to it, and brings the next tiles.
+// Between two barriers, while the outputs are stored, it replaces tiles and state.  As eight
+// waves the two shorter chains of a chunk run at once and fit 128 registers, four waves a
+// SIMD; one group doing both took 1.6 times as long (forwards at head_dim 64, and more
+// backwards).
+// Products are formed transposed (Y X^T, then Z^T P^T), so that P leaves the accumulators as
+// the next product's operand and a lane stores four neighbouring values of one token.
 // P and S are taken as two bf16 terms (three for the sums r, which are fp32 results), so
 // that the output is rounded once.
 // Pair weights: inside the wave's own 16 tokens each from its two gate sums; with an earlier
@@ -477,7 +490,7 @@ constexpr int walk_lds() {
     return (GC * D + GC * EB + (sizeof(E) == 4 ? 1 : DOT ? 3 : 2) * EB * D) * (int)sizeof(E) + GATE_ROWS * GC * 4;
 }
 
-template <typename E, int D, int EB, bool REV, bool DOT>
+template <typename E, int D, int EB, bool REV, bool DOT, bool SPLIT>
 __device__ __forceinline__ void walk(const Walk& w, int id, char* lds) {
     using TY = Tile<E, D>;
     using TZ = Tile<E, EB>;
@@ -494,8 +507,8 @@ __device__ __forceinline__ void walk(const Walk& w, int id, char* lds) {
     const float* rw = kw + GC;
     const float* cw = rw + GC;
 
-    const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, li = lane & 15,
-              lg = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) & 3;         // in its group
+    const int tid = threadIdx.x & (THREADS - 1), lane = tid & 63, li = lane & 15, lg = lane >> 4;
     constexpr int NB = D / EB;
     const int eb = id % NB;
     id /= NB;
@@ -508,13 +521,106 @@ __device__ __forceinline__ void walk(const Walk& w, int id, char* lds) {
     if (w.lens) len = min(max(w.lens[b], 0), T);
     const int c0 = seg * w.seg_chunks, c1 = min(c0 + w.seg_chunks, (T + GC - 1) / GC);
     const int live_end = min(c1, (len + GC - 1) / GC);   // chunks from here on hold no live token
-    const int hx_all = w.HK * w.nx;
     const int64_t tok0 = (int64_t)b * T;
-    float* const rout = DOT ? w.r + (int64_t)eb * w.B * T * hx_all : nullptr;
+    const int chunks = max(live_end - c0, 0);
+    const int first = REV ? live_end - 1 : c0, dir = REV ? -1 : 1;
+    const int nx = REV ? 1 : w.nx, ny = REV ? w.ny : 1;   // backwards it is Y and Z that a group has several of
+    const bool keep = w.end && (REV ? seg == 0 : seg == w.nseg - 1);   // the state after the last chunk is wanted
+    constexpr int ES = (int)sizeof(E);
+    constexpr bool FRESH = D == 128;
 
+    // ---- the state's part: tiles, gates and the state
     typename ST::Acc S;
-    load_state<D, EB>(S, w.start ? w.start + ((int64_t)b * w.HK + hk) * w.start_pair + seg * w.start_seg + eb * EB * w.se : nullptr,
-                      w.sc, w.se, wave, lane);
+    Staged<E, D> ys;
+    Staged<E, EB> zs;
+    float graw = 0.f, eh = 0.f, ef = 0.f;
+    Gates gs = {0.f, 0.f};
+    // a chunk past the walk's end has no rows
+    auto fetch = [&](int ci, int hy) {
+        const int c = first + dir * ci;
+        const int live = ci < chunks ? min(len - c * GC, GC) : 0;
+        const int64_t tk = tok0 + (int64_t)c * GC;
+        const int h = hk * ny + hy;
+        ys.load(rows_of<E>(w.y.p, tk, w.y.stride, h * D, live, D), (int)w.y.stride, tid);
+        zs.load(rows_of<E>(w.z.p, tk, w.z.stride, h * D + eb * EB, live, EB), (int)w.z.stride, tid);
+        graw = __int_as_float(__builtin_amdgcn_raw_buffer_load_b32(rows_of<float>(w.g, tk, w.HK, hk, live, 1), lane * w.HK * 4, 0, 0));
+    };
+    auto next_gates = [&]() {
+        gs = gate_sums(graw);
+        eh = lane_value(gs.h, 63);
+        ef = lane_value(gs.f, 63);
+    };
+    auto begin_state = [&]() {
+        load_state<D, EB>(S, w.start ? w.start + ((int64_t)b * w.HK + hk) * w.start_pair + seg * w.start_seg + eb * EB * w.se : nullptr,
+                          w.sc, w.se, wave, lane);
+        fetch(0, 0);
+        next_gates();
+    };
+    auto put_tiles = [&]() {
+        ys.store(yt, tid);
+        zs.store(zt, tid);
+    };
+    auto publish = [&](int at) {
+        put_gates<REV>(gh, gs, eh, ef, w.pair_scale, w.row_scale, w.key_scale, wave, at);
+#pragma unroll
+        for (int a = 0; a < ST::CW; ++a)
+#pragma unroll
+            for (int e = 0; e < ST::EW; ++e)
+                put4<E, D, NS>(stt, SB, state_row(16 * ST::et(wave, e) + (at & 15)), 16 * ST::ct(wave, a) + 4 * (at >> 4), S[a][e]);
+    };
+    auto end_state = [&]() {
+        if (keep)
+            store_state<D, EB>(S, w.end + ((int64_t)b * w.HK + hk) * D * D + eb * EB * w.se, w.sc, w.se, wave, lane);
+    };
+
+    if constexpr (SPLIT) {
+        if (__builtin_amdgcn_readfirstlane(threadIdx.x >> 8) != 0) {
+            begin_state();
+            if (chunks > 0) {
+                put_tiles();
+                publish(lane);
+                __syncthreads();
+            }
+            for (int ci = 0; ci < chunks; ++ci) {
+                float decay = pow2(eh + ef);
+                for (int hy = 0; hy < ny; ++hy) {
+                    const bool last_y = hy + 1 == ny;
+                    const int at = in_loop<FRESH>(lane);
+                    fetch(last_y ? ci + 1 : ci, last_y ? 0 : hy + 1);
+                    if (keep || ci + 1 < chunks) update_state<E, D, EB>(S, yt, zt, kw, decay, wave, at);
+                    decay = 1.f;
+                    if (last_y) next_gates();
+                    __syncthreads();              // the tiles' and the state's reads are over
+                    put_tiles();
+                    if (last_y) publish(at);
+                    __syncthreads();
+                }
+            }
+            end_state();
+            return;
+        }
+    }
+
+    // ---- the rows' part
+    const int hx_all = w.HK * w.nx;
+    float* const rout = DOT ? w.r + (int64_t)eb * w.B * T * hx_all : nullptr;
+    const int tl = 16 * wave + li;                        // this lane's token in a chunk
+    Frag<E> xf[KD], x2f[DOT ? KE : 1];
+    auto fetch_x = [&](int ci, int hx, Frag<E> (&x)[KD], Frag<E> (&x2)[DOT ? KE : 1]) {
+        const int c = first + dir * ci;
+        const int live = ci < chunks ? min(len - c * GC, GC) : 0;
+        const int64_t tk = tok0 + (int64_t)c * GC;
+        const int h = hk * nx + hx;
+        const __amdgpu_buffer_rsrc_t rx = rows_of<E>(w.x.p, tk, w.x.stride, h * D, live, D);
+#pragma unroll
+        for (int kk = 0; kk < KD; ++kk) load_row(rx, (tl * (int)w.x.stride + 8 * lg + 32 * kk) * ES, x[kk]);
+        if constexpr (DOT) {
+            const __amdgpu_buffer_rsrc_t r2 = rows_of<E>(w.x2.p, tk, w.x2.stride, h * D + eb * EB, live, EB);
+#pragma unroll
+            for (int kk = 0; kk < KE; ++kk) load_row(r2, (tl * (int)w.x2.stride + 8 * lg + 32 * kk) * ES, x2[kk]);
+        }
+    };
+    fetch_x(0, 0, xf, x2f);
 
     // rows of dead chunks are zero
     {
@@ -530,203 +636,174 @@ __device__ __forceinline__ void walk(const Walk& w, int id, char* lds) {
         }
     }
 
-    const int chunks = max(live_end - c0, 0);
-    const int first = REV ? live_end - 1 : c0, dir = REV ? -1 : 1;
-    const int nx = REV ? 1 : w.nx, ny = REV ? w.ny : 1;   // backwards it is Y and Z that a group has several of
-    const int tl = 16 * wave + li;                        // this lane's token in a chunk
-    constexpr int ES = (int)sizeof(E);
-    Staged<E, D> ys;
-    Staged<E, EB> zs;
-    float graw = 0.f;
-    // a chunk past the walk's end has no rows
-    auto fetch = [&](int ci, int hy) {
-        const int c = first + dir * ci;
-        const int live = ci < chunks ? min(len - c * GC, GC) : 0;
-        const int64_t tk = tok0 + (int64_t)c * GC;
-        const int h = hk * ny + hy;
-        ys.load(rows_of<E>(w.y.p, tk, w.y.stride, h * D, live, D), (int)w.y.stride, tid);
-        zs.load(rows_of<E>(w.z.p, tk, w.z.stride, h * D + eb * EB, live, EB), (int)w.z.stride, tid);
-        graw = __int_as_float(__builtin_amdgcn_raw_buffer_load_b32(rows_of<float>(w.g, tk, w.HK, hk, live, 1), lane * w.HK * 4, 0, 0));
-    };
-    // x2 in row order for its product with Z, and in token order, as the accumulators hold the output
-    Frag<E> xf[KD], x2f[DOT ? KE : 1], x2t[DOT ? KE : 1];
-    auto fetch_x = [&](int ci, int hx, Frag<E> (&x)[KD], Frag<E> (&x2)[DOT ? KE : 1], Frag<E> (&xt)[DOT ? KE : 1]) {
-        const int c = first + dir * ci;
-        const int live = ci < chunks ? min(len - c * GC, GC) : 0;
-        const int64_t tk = tok0 + (int64_t)c * GC;
-        const int h = hk * nx + hx;
-        const __amdgpu_buffer_rsrc_t rx = rows_of<E>(w.x.p, tk, w.x.stride, h * D, live, D);
-#pragma unroll
-        for (int kk = 0; kk < KD; ++kk) load_row(rx, (tl * (int)w.x.stride + 8 * lg + 32 * kk) * ES, x[kk]);
-        if constexpr (DOT) {
-            const __amdgpu_buffer_rsrc_t r2 = rows_of<E>(w.x2.p, tk, w.x2.stride, h * D + eb * EB, live, EB);
-#pragma unroll
-            for (int kk = 0; kk < KE; ++kk) {
-                load_row(r2, (tl * (int)w.x2.stride + 8 * lg + 32 * kk) * ES, x2[kk]);
-                load_row_t(r2, (tl * (int)w.x2.stride + 4 * lg + 32 * kk) * ES, xt[kk]);
-            }
-        }
-    };
-    fetch(0, 0);
-    fetch_x(0, 0, xf, x2f, x2t);
-
-    const bool keep = w.end && (REV ? seg == 0 : seg == w.nseg - 1);   // the state after the last chunk is wanted
     f32x4 o[ET];
     float rsum = 0.f;
-    for (int ci = 0; ci < chunks; ++ci) {
+            auto store_rows = [&](int ci, int hx) {
         const int c = first + dir * ci;
         const bool live = c * GC + tl < len, whole = (c + 1) * GC <= len;
         const int rows = min(T - c * GC, GC);
         const int64_t tk0 = tok0 + (int64_t)c * GC;
-        const Gates gs = gate_sums(graw);
-        const float eh = lane_value(gs.h, 63), ef = lane_value(gs.f, 63);
-        float decay = pow2(eh + ef);
-        for (int hy = 0; hy < ny; ++hy) {
-            __syncthreads();                      // the last tile's reads are over
-            ys.store(yt, tid);
-            zs.store(zt, tid);
-            if (!REV || hy == 0) {
-                put_gates<REV>(gh, gs, eh, ef, w.pair_scale, w.row_scale, w.key_scale, wave, lane);
-#pragma unroll
-                for (int a = 0; a < ST::CW; ++a)
-#pragma unroll
-                    for (int e = 0; e < ST::EW; ++e)
-                        put4<E, D, NS>(stt, SB, 16 * ST::et(wave, e) + li, 16 * ST::ct(wave, a) + 4 * lg, S[a][e]);
-            }
-            __syncthreads();
-            const bool last_y = hy + 1 == ny;
-            fetch(last_y ? ci + 1 : ci, last_y ? 0 : hy + 1);
-
-            const float th = gh[tl], tf = gh[GC + tl], trw = rw[tl];
-            for (int hx = 0; hx < nx; ++hx) {
-                const bool last_x = hx + 1 == nx;
-                asm volatile("" ::: "memory");    // reads of the tiles stay in the loop: hoisted, they fill the registers
-                Frag<E> xn[KD], x2n[DOT ? KE : 1], xtn[DOT ? KE : 1];
-                if (!REV || last_y) fetch_x(last_x ? ci + 1 : ci, last_x ? 0 : hx + 1, xn, x2n, xtn);
-                if (!REV || hy == 0) {
-                    // from the state: o = S^T x
-                    rsum = 0.f;
-#pragma unroll
-                    for (int e = 0; e < ET; ++e) {
-                        f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                        for (int n = NS - 1; n >= 0; --n)
-#pragma unroll
-                            for (int kk = 0; kk < KD; ++kk)
-                                acc = mma(TY::rows(stt + n * SB, 16 * e, kk, lane), xf[kk], acc);
-                        o[e] = acc * trw;
-                    }
-                    if constexpr (DOT) {
-#pragma unroll
-                        for (int kk = 0; kk < KE; ++kk) {
-                            float u[8];
-                            widen(x2t[kk], u);
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) rsum += u[j] * o[2 * kk][j] + u[4 + j] * o[2 * kk + 1][j];
-                        }
-                    }
-                }
-                // weights of the tokens s of the chunk: groups of 16 that come before (after) the wave's own,
-                // the others' weight being 0, and its own
-                float p[GC / 16][4];
-#pragma unroll
-                for (int st = 0; st < GC / 16; ++st) {
-                    if (st == (REV ? 0 : GC / 16 - 1)) {
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) p[st][j] = 0.f;
-                        continue;
-                    }
-                    f32x4 acc = {0.f, 0.f, 0.f, 0.f}, m = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                    for (int k = 0; k < KD; ++k) acc = mma(TY::rows(yt, 16 * st, k, lane), xf[k], acc);
-                    if constexpr (DOT) {
-#pragma unroll
-                        for (int k = 0; k < KE; ++k) m = mma(TZ::rows(zt, 16 * st, k, lane), x2f[k], m);
-                    }
-                    const float rf = group_factor<REV>(gh, th, tf, st, wave);
-                    const f32x4 cs = *reinterpret_cast<const f32x4*>(cw + 16 * st + 4 * lg);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        p[st][j] = acc[j] * (cs[j] * rf);
-                        if constexpr (DOT) rsum += p[st][j] * m[j];
-                    }
-                }
-                {
-                    f32x4 acc = {0.f, 0.f, 0.f, 0.f}, m = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                    for (int k = 0; k < KD; ++k) acc = mma(TY::rows(yt, 16 * wave, k, lane), xf[k], acc);
-                    if constexpr (DOT) {
-#pragma unroll
-                        for (int k = 0; k < KE; ++k) m = mma(TZ::rows(zt, 16 * wave, k, lane), x2f[k], m);
-                    }
-                    const f32x4 ow = own_weights<REV>(gh, th, tf, w.pair_scale, wave, lane);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int s = 4 * lg + j;
-                        const float v = acc[j] * ow[j];
-                        const float own = (REV ? s >= li : s <= li) ? v : 0.f;
-                        if constexpr (DOT) rsum += s != li ? own * m[j] : 0.f;
-#pragma unroll
-                        for (int st = 0; st < GC / 16; ++st) p[st][j] = st == wave ? own : p[st][j];
-                    }
-                }
-#pragma unroll
-                for (int kk = 0; kk < GC / 32; ++kk) {
-                    float q[8];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        q[j] = p[2 * kk][j];
-                        q[4 + j] = p[2 * kk + 1][j];
-                    }
-                    Frag<E> pf[NP];
-                    split<NP>(q, pf);
-#pragma unroll
-                    for (int e = 0; e < ET; ++e) {
-                        const Frag<E> z = TZ::cols(zt, kk, e, lane);
-#pragma unroll
-                        for (int n = NP - 1; n >= 0; --n) o[e] = mma(z, pf[n], o[e]);
-                    }
-                }
-                if (!REV || last_y) {
-                    const int h = hk * nx + hx;
-                    const __amdgpu_buffer_rsrc_t ro = rows_of<E>(w.out, tk0, (int64_t)hx_all * D, h * D + eb * EB, rows, EB);
-                    if (!whole) {
-#pragma unroll
-                        for (int e = 0; e < ET; ++e)
-                            if (!live) o[e] = f32x4{0.f, 0.f, 0.f, 0.f};
-                    }
-#pragma unroll
+                const int h = hk * nx + hx;
+                const __amdgpu_buffer_rsrc_t ro = rows_of<E>(w.out, tk0, (int64_t)hx_all * D, h * D + eb * EB, rows, EB);
+                if (!whole) {
+    #pragma unroll
                     for (int e = 0; e < ET; ++e)
-                        store_row4(ro, (tl * hx_all * D + 16 * e + 4 * lg) * ES, o[e], E());
-                    if constexpr (DOT) {
-                        float s = rsum + shfl_xor(rsum, 16);
-                        s += shfl_xor(s, 32);     // all four lanes of a token store the same sum
-                        const __amdgpu_buffer_rsrc_t rr = rows_of<float>(rout, tk0, hx_all, h, rows, 1);
-                        __builtin_amdgcn_raw_buffer_store_b32(__float_as_int(live ? s : 0.f), rr, tl * hx_all * 4, 0, 0);
-                    }
-#pragma unroll
-                    for (int kk = 0; kk < KD; ++kk) xf[kk] = xn[kk];
-                    if constexpr (DOT) {
-#pragma unroll
-                        for (int kk = 0; kk < KE; ++kk) {
-                            x2f[kk] = x2n[kk];
-                            x2t[kk] = xtn[kk];
-                        }
-                    }
+                        if (!live) o[e] = f32x4{0.f, 0.f, 0.f, 0.f};
                 }
+    #pragma unroll
+                for (int k = 0; k < KE; ++k)
+                    store_row8(ro, (tl * hx_all * D + 32 * k + 8 * lg) * ES, o[2 * k], o[2 * k + 1], E());
+                if constexpr (DOT) {
+                    float s = rsum + shfl_xor(rsum, 16);
+                    s += shfl_xor(s, 32);             // all four lanes of a token store the same sum
+                    const __amdgpu_buffer_rsrc_t rr = rows_of<float>(rout, tk0, hx_all, h, rows, 1);
+                    __builtin_amdgcn_raw_buffer_store_b32(__float_as_int(live ? s : 0.f), rr, tl * hx_all * 4, 0, 0);
+                }
+            };
+    // the outputs of the tiles in LDS, all heads of X; all but the last head's are stored
+    auto compute_rows = [&](int ci, int hy) {
+        const bool last_y = hy + 1 == ny;
+                    const float th = gh[tl], tf = gh[GC + tl], trw = rw[tl];
+                    for (int hx = 0; hx < nx; ++hx) {
+                        const bool last_x = hx + 1 == nx;
+                        const int at = in_loop<FRESH>(lane);
+                        Frag<E> xn[KD], x2n[DOT ? KE : 1];
+                        if (!REV || last_y) fetch_x(last_x ? ci + 1 : ci, last_x ? 0 : hx + 1, xn, x2n);
+                        if (!REV || hy == 0) {
+                            // from the state: o = S^T x
+                            rsum = 0.f;
+        #pragma unroll
+                            for (int e = 0; e < ET; ++e) {
+                                f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+        #pragma unroll
+                                for (int n = NS - 1; n >= 0; --n)
+        #pragma unroll
+                                    for (int kk = 0; kk < KD; ++kk)
+                                        acc = mma(TY::rows(stt + n * SB, 16 * e, kk, at), xf[kk], acc);
+                                o[e] = acc * trw;
+                            }
+                            if constexpr (DOT) {
+        #pragma unroll
+                                for (int kk = 0; kk < KE; ++kk) {
+                                    float u[8];
+                                    widen(x2f[kk], u);
+        #pragma unroll
+                                    for (int j = 0; j < 4; ++j) rsum += u[j] * o[2 * kk][j] + u[4 + j] * o[2 * kk + 1][j];
+                                }
+                            }
+                        }
+                        // the chunk's tokens s, 32 at a time: the row's own group of 16 and the groups that come before
+                        // (backwards: after) it, the others' weight being 0
+                        float own[4];
+                        {
+                            f32x4 acc = {0.f, 0.f, 0.f, 0.f}, m = {0.f, 0.f, 0.f, 0.f};
+        #pragma unroll
+                            for (int k = 0; k < KD; ++k) acc = mma(TY::rows(yt, 16 * wave, k, at), xf[k], acc);
+                            if constexpr (DOT) {
+        #pragma unroll
+                                for (int k = 0; k < KE; ++k) m = mma(TZ::rows(zt, 16 * wave, k, at), x2f[k], m);
+                            }
+                            const f32x4 ow = own_weights<REV>(gh, th, tf, w.pair_scale, wave, lane);
+        #pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                const int s = 4 * lg + j;
+                                const float v = acc[j] * ow[j];
+                                own[j] = (REV ? s >= li : s <= li) ? v : 0.f;
+                                if constexpr (DOT) rsum += s != li ? own[j] * m[j] : 0.f;
+                            }
+                        }
+        #pragma unroll
+                        for (int kk = 0; kk < GC / 32; ++kk) {
+                            float q[8];
+        #pragma unroll
+                            for (int u = 0; u < 2; ++u) {
+                                const int st = 2 * kk + u;
+                                if (st == (REV ? 0 : GC / 16 - 1)) {      // no row's other group
+        #pragma unroll
+                                    for (int j = 0; j < 4; ++j) q[4 * u + j] = st == wave ? own[j] : 0.f;
+                                    continue;
+                                }
+                                f32x4 acc = {0.f, 0.f, 0.f, 0.f}, m = {0.f, 0.f, 0.f, 0.f};
+        #pragma unroll
+                                for (int k = 0; k < KD; ++k) acc = mma(TY::rows(yt, 16 * st, k, at), xf[k], acc);
+                                if constexpr (DOT) {
+        #pragma unroll
+                                    for (int k = 0; k < KE; ++k) m = mma(TZ::rows(zt, 16 * st, k, at), x2f[k], m);
+                                }
+                                const float rf = group_factor<REV>(gh, th, tf, st, wave);
+                                const f32x4 cs = *reinterpret_cast<const f32x4*>(cw + 16 * st + 4 * lg);
+        #pragma unroll
+                                for (int j = 0; j < 4; ++j) {
+                                    const float v = acc[j] * (cs[j] * rf);
+                                    if constexpr (DOT) rsum += v * m[j];
+                                    q[4 * u + j] = st == wave ? own[j] : v;
+                                }
+                            }
+                            Frag<E> pf[NP];
+                            split<NP>(q, pf);
+        #pragma unroll
+                            for (int e = 0; e < ET; ++e) {
+                                const Frag<E> z = TZ::template cols<true>(zt, kk, e, at);
+        #pragma unroll
+                                for (int n = NP - 1; n >= 0; --n) o[e] = mma(z, pf[n], o[e]);
+                            }
+                        }
+                        if (!REV || last_y) {
+        #pragma unroll
+                            for (int kk = 0; kk < KD; ++kk) xf[kk] = xn[kk];
+                            if constexpr (DOT) {
+        #pragma unroll
+                                for (int kk = 0; kk < KE; ++kk) x2f[kk] = x2n[kk];
+                            }
+                        }
+                        if (!last_x) store_rows(ci, hx);
+                    }
+    };
+    if constexpr (SPLIT) {
+        if (chunks > 0) __syncthreads();
+        for (int ci = 0; ci < chunks; ++ci)
+            for (int hy = 0; hy < ny; ++hy) {
+                compute_rows(ci, hy);
+                __syncthreads();                  // the tiles' and the state's reads are over
+                if (!REV || hy + 1 == ny) store_rows(ci, nx - 1);
+                __syncthreads();
             }
-            if (keep || ci + 1 < chunks) update_state<E, D, EB>(S, yt, zt, kw, decay, wave, lane);
-            decay = 1.f;
+    } else {
+        begin_state();
+        for (int ci = 0; ci < chunks; ++ci) {
+            float decay = pow2(eh + ef);
+            for (int hy = 0; hy < ny; ++hy) {
+                const bool last_y = hy + 1 == ny;
+                __syncthreads();                  // the tiles' and the state's reads are over
+                put_tiles();
+                if (hy == 0) publish(lane);
+                __syncthreads();
+                fetch(last_y ? ci + 1 : ci, last_y ? 0 : hy + 1);
+                compute_rows(ci, hy);
+                if (!REV || last_y) store_rows(ci, nx - 1);
+                if (keep || ci + 1 < chunks) update_state<E, D, EB>(S, yt, zt, kw, decay, wave, lane);
+                decay = 1.f;
+                if (last_y) next_gates();
+            }
         }
+        end_state();
     }
-    if (keep)
-        store_state<D, EB>(S, w.end + ((int64_t)b * w.HK + hk) * D * D + eb * EB * w.se, w.sc, w.se, wave, lane);
 }
 
+// At D = 128 in bf16 one group of waves does both parts in turn: split, the rows' part does
+// not fit 128 registers, and past them a compute unit holds one workgroup of eight waves
+// instead of two of four (backwards, 2 x 4097 tokens, 12 heads over 4: 117 us, split 148).
+// In fp32 either way it holds one, and eight waves are better than four (forwards, 4 x 2048
+// tokens, 8 heads: 111 us, not split 125).
+template <typename E, int D>
+constexpr bool split_walk() { return D <= 64 || sizeof(E) == 4; }
+template <typename E, int D>
+constexpr int walk_threads() { return split_walk<E, D>() ? 2 * THREADS : THREADS; }
+
 template <typename E, int D, int EB>
-__global__ void __launch_bounds__(THREADS, sizeof(E) == 2 || D <= 64 ? 2 : 1) gated_walk(Walk w) {
+__global__ void __launch_bounds__((walk_threads<E, D>()), (!split_walk<E, D>() || D == 128 ? 2 : 4)) gated_walk(Walk w) {
     __shared__ __attribute__((aligned(16))) char lds[walk_lds<E, D, EB, false>()];
-    walk<E, D, EB, false, false>(w, xcd_run(blockIdx.x, gridDim.x), lds);
+    walk<E, D, EB, false, false, split_walk<E, D>()>(w, xcd_run(blockIdx.x, gridDim.x), lds);
 }
 
 // ---------------------------------------------------------------- dk and dv together
@@ -735,6 +812,8 @@ __global__ void __launch_bounds__(THREADS, sizeof(E) == 2 || D <= 64 ? 2 : 1) ga
 // summed once, where two walks would do each twice.  D lies in LDS once, transposed ([e][c]):
 // dv contracts it over c (its columns), dk over e (its rows, by transposing reads).  D <= 64: at 128 the state of all columns leaves room for one
 // workgroup of a compute unit, and dk and dv are walks of their own.
+// One group of waves computes dk and k . dk and brings the tiles of q, the other dv, with D
+// in its accumulators, and the tiles of do.
 struct Back {
     Role q, k, v, dout;
     void* dk;
@@ -742,7 +821,7 @@ struct Back {
     float* r;            // k . dk without a token's own term, [B, T, HK]
     const float* g;
     const int32_t* lens;
-    const float* start;  // gradient of the state behind each segment, [B*HK][nseg][D*D]
+    const float* start;  // gradient of the state behind each segment, [B*HK][nseg][D*D], or nullptr (zero)
     float* end;          // gradient of the initial state, or nullptr
     int B, T, HK, G, nseg, seg_chunks;
     float scale;
@@ -765,8 +844,9 @@ __device__ __forceinline__ void back(const Back& w, int id, char* lds) {
     const float* rw = kw + GC;
     const float* cw = rw + GC;
 
-    const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, li = lane & 15,
-              lg = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) & 3;         // in its group
+    const bool dk_group = __builtin_amdgcn_readfirstlane(threadIdx.x >> 8) == 0;
+    const int tid = threadIdx.x & (THREADS - 1), lane = tid & 63, li = lane & 15, lg = lane >> 4;
     const int hk = id % w.HK;
     id /= w.HK;
     const int seg = id % w.nseg, b = id / w.nseg;
@@ -776,200 +856,265 @@ __device__ __forceinline__ void back(const Back& w, int id, char* lds) {
     const int c0 = seg * w.seg_chunks, c1 = min(c0 + w.seg_chunks, (T + GC - 1) / GC);
     const int live_end = min(c1, (len + GC - 1) / GC);
     const int64_t tok0 = (int64_t)b * T, pair = (int64_t)b * w.HK + hk;
+    const int chunks = max(live_end - c0, 0);
+    const int tl = 16 * wave + li;
+    const bool keep = w.end && seg == 0;
+    constexpr bool FRESH = true;
 
-    typename ST::Acc S;
-    load_state<D, D>(S, w.start + (pair * w.nseg + seg) * D * D, D, 1, wave, lane);
-
-    {   // rows of dead chunks are zero
+    // k or v of a chunk's rows, this lane's token; a chunk past the walk's end has no rows
+    auto fetch_x = [&](int ci, const Role& x, Frag<E> (&f)[KD]) {
+        const int c = live_end - 1 - ci;
+        const int live = ci < chunks ? min(len - c * GC, GC) : 0;
+        const __amdgpu_buffer_rsrc_t r = rows_of<E>(x.p, tok0 + (int64_t)c * GC, x.stride, hk * D, live, D);
+#pragma unroll
+        for (int kk = 0; kk < KD; ++kk) load_row(r, (tl * (int)x.stride + 8 * lg + 32 * kk) * ES, f[kk]);
+    };
+    auto store_rows = [&](int c, void* out, f32x4 (&o)[DT]) {
+        const __amdgpu_buffer_rsrc_t r = rows_of<E>(out, tok0 + (int64_t)c * GC, (int64_t)w.HK * D, hk * D, min(T - c * GC, GC), D);
+        if ((c + 1) * GC > len) {
+#pragma unroll
+            for (int e = 0; e < DT; ++e)
+                if (c * GC + tl >= len) o[e] = f32x4{0.f, 0.f, 0.f, 0.f};
+        }
+#pragma unroll
+        for (int k = 0; k < KD; ++k) store_row8(r, (tl * w.HK * D + 32 * k + 8 * lg) * ES, o[2 * k], o[2 * k + 1], E());
+    };
+    // rows of dead chunks are zero
+    auto zero_rows = [&](void* out) {
         const int t0 = max(c0, live_end) * GC, n = min(c1 * GC, T) - t0;
         constexpr int PC = D / 4;
         const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
-        for (int p = tid; p < n * PC; p += THREADS) {
-            const int64_t tk = tok0 + t0 + p / PC, at = (tk * w.HK + hk) * D + (p % PC) * 4;
-            store4(static_cast<E*>(w.dk) + at, zero);
-            store4(static_cast<E*>(w.dv) + at, zero);
-            if (p % PC == 0) w.r[tk * w.HK + hk] = 0.f;
+        for (int p = tid; p < n * PC; p += THREADS)
+            store4(static_cast<E*>(out) + ((tok0 + t0 + p / PC) * w.HK + hk) * D + (p % PC) * 4, zero);
+    };
+    // The row's own group of 16 tokens: t >= this one
+    auto own_pairs = [&](const f32x4& a, const f32x4& ow, float (&o)[4]) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[j] = 4 * lg + j >= li ? a[j] * ow[j] : 0.f;
+    };
+
+    if (!dk_group) {
+        typename ST::Acc S;
+        load_state<D, D>(S, w.start ? w.start + (pair * w.nseg + seg) * D * D : nullptr, D, 1, wave, lane);
+        Staged<E, D> zs;
+        float graw = 0.f;
+        auto fetch = [&](int ci, int hy) {
+            const int c = live_end - 1 - ci;
+            const int live = ci < chunks ? min(len - c * GC, GC) : 0;
+            const int64_t tk = tok0 + (int64_t)c * GC;
+            zs.load(rows_of<E>(w.dout.p, tk, w.dout.stride, (hk * w.G + hy) * D, live, D), (int)w.dout.stride, tid);
+            graw = __int_as_float(__builtin_amdgcn_raw_buffer_load_b32(rows_of<float>(w.g, tk, w.HK, hk, live, 1), lane * w.HK * 4, 0, 0));
+        };
+        fetch(0, 0);
+        Frag<E> kf[KD], kn[KD];
+        fetch_x(0, w.k, kf);
+        zero_rows(w.dv);
+        Gates gs = gate_sums(graw);
+        float eh = lane_value(gs.h, 63), ef = lane_value(gs.f, 63);
+        auto publish = [&](int at) {
+            put_gates<true>(gh, gs, eh, ef, w.scale, 1.f, w.scale, wave, at);
+#pragma unroll
+            for (int a = 0; a < ST::CW; ++a)
+#pragma unroll
+                for (int e = 0; e < ST::EW; ++e)
+                    put4<E, D, NS>(stt, SB, state_row(16 * ST::et(wave, e) + (at & 15)), 16 * ST::ct(wave, a) + 4 * (at >> 4), S[a][e]);
+        };
+        if (chunks > 0) {
+            zs.store(zt, tid);
+            publish(lane);
+            __syncthreads();
         }
+        f32x4 ov[DT];
+        for (int ci = 0; ci < chunks; ++ci) {
+            float decay = pow2(eh + ef);
+            for (int hy = 0; hy < w.G; ++hy) {
+                const bool last = hy + 1 == w.G;
+                const int at = in_loop<FRESH>(lane);
+                fetch(last ? ci + 1 : ci, last ? 0 : hy + 1);
+                if (hy == 0) {
+                    fetch_x(ci + 1, w.k, kn);
+                    // from the state: dv = D^T k
+                    const float trw = rw[tl];
+#pragma unroll
+                    for (int e = 0; e < DT; ++e) {
+                        f32x4 a = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                        for (int n = NSV - 1; n >= 0; --n)
+#pragma unroll
+                            for (int kk = 0; kk < KD; ++kk) a = mma(TL::rows(stt + n * SB, 16 * e, kk, at), kf[kk], a);
+                        ov[e] = a * trw;
+                    }
+                }
+                const float th = gh[tl], tf = gh[GC + tl];
+                float pown[4];
+                {
+                    f32x4 a = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int k = 0; k < KD; ++k) a = mma(TL::rows(yt, 16 * wave, k, at), kf[k], a);
+                    own_pairs(a, own_weights<true>(gh, th, tf, w.scale, wave, lane), pown);
+                }
+#pragma unroll
+                for (int kk = 0; kk < GC / 32; ++kk) {
+                    float pq[8];
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        const int st = 2 * kk + u;
+                        if (st == 0) {            // no row's other group
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) pq[j] = wave == 0 ? pown[j] : 0.f;
+                            continue;
+                        }
+                        f32x4 a = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                        for (int k = 0; k < KD; ++k) a = mma(TL::rows(yt, 16 * st, k, at), kf[k], a);
+                        const float rf = group_factor<true>(gh, th, tf, st, wave);
+                        const f32x4 cs = *reinterpret_cast<const f32x4*>(cw + 16 * st + 4 * lg);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) pq[4 * u + j] = st == wave ? pown[j] : a[j] * (cs[j] * rf);
+                    }
+                    Frag<E> pf[NP];
+                    split<NP>(pq, pf);
+#pragma unroll
+                    for (int e = 0; e < DT; ++e) {
+                        const Frag<E> z = TL::template cols<true>(zt, kk, e, at);
+#pragma unroll
+                        for (int n = NP - 1; n >= 0; --n) ov[e] = mma(z, pf[n], ov[e]);
+                    }
+                }
+                if (keep || ci + 1 < chunks) update_state<E, D, D>(S, yt, zt, kw, decay, wave, at);
+                decay = 1.f;
+                if (last) {
+                    gs = gate_sums(graw);
+                    eh = lane_value(gs.h, 63);
+                    ef = lane_value(gs.f, 63);
+                }
+                __syncthreads();                  // the tiles' and the state's reads are over
+                zs.store(zt, tid);
+                if (last) publish(at);
+                __syncthreads();
+            }
+            store_rows(live_end - 1 - ci, w.dv, ov);
+#pragma unroll
+            for (int kk = 0; kk < KD; ++kk) kf[kk] = kn[kk];
+        }
+        if (keep) store_state<D, D>(S, w.end + pair * D * D, D, 1, wave, lane);
+        return;
     }
 
-    const int chunks = max(live_end - c0, 0);
-    const int tl = 16 * wave + li;
-    Staged<E, D> ys, zs;
-    float graw = 0.f;
+    Staged<E, D> ys;
     auto fetch = [&](int ci, int hy) {
         const int c = live_end - 1 - ci;
         const int live = ci < chunks ? min(len - c * GC, GC) : 0;
-        const int64_t tk = tok0 + (int64_t)c * GC;
-        const int h = hk * w.G + hy;
-        ys.load(rows_of<E>(w.q.p, tk, w.q.stride, h * D, live, D), (int)w.q.stride, tid);
-        zs.load(rows_of<E>(w.dout.p, tk, w.dout.stride, h * D, live, D), (int)w.dout.stride, tid);
-        graw = __int_as_float(__builtin_amdgcn_raw_buffer_load_b32(rows_of<float>(w.g, tk, w.HK, hk, live, 1), lane * w.HK * 4, 0, 0));
-    };
-    // k also in token order, as the accumulators hold dk
-    Frag<E> kf[KD], kt[KD], vf[KD], kn[KD], ktn[KD], vn[KD];
-    auto fetch_x = [&](int ci, Frag<E> (&k)[KD], Frag<E> (&kt)[KD], Frag<E> (&v)[KD]) {
-        const int c = live_end - 1 - ci;
-        const int live = ci < chunks ? min(len - c * GC, GC) : 0;
-        const int64_t tk = tok0 + (int64_t)c * GC;
-        const __amdgpu_buffer_rsrc_t rk = rows_of<E>(w.k.p, tk, w.k.stride, hk * D, live, D);
-        const __amdgpu_buffer_rsrc_t rv = rows_of<E>(w.v.p, tk, w.v.stride, hk * D, live, D);
-#pragma unroll
-        for (int kk = 0; kk < KD; ++kk) {
-            load_row(rk, (tl * (int)w.k.stride + 8 * lg + 32 * kk) * ES, k[kk]);
-            load_row_t(rk, (tl * (int)w.k.stride + 4 * lg + 32 * kk) * ES, kt[kk]);
-            load_row(rv, (tl * (int)w.v.stride + 8 * lg + 32 * kk) * ES, v[kk]);
-        }
+        ys.load(rows_of<E>(w.q.p, tok0 + (int64_t)c * GC, w.q.stride, (hk * w.G + hy) * D, live, D), (int)w.q.stride, tid);
     };
     fetch(0, 0);
-    fetch_x(0, kf, kt, vf);
-
-    const bool keep = w.end && seg == 0;
-    f32x4 ok[DT], ov[DT];
+    Frag<E> kf[KD], vf[KD], kn[KD], vn[KD];
+    fetch_x(0, w.k, kf);
+    fetch_x(0, w.v, vf);
+    zero_rows(w.dk);
+    for (int t = max(c0, live_end) * GC + tid; t < min(c1 * GC, T); t += THREADS) w.r[(tok0 + t) * w.HK + hk] = 0.f;
+    f32x4 ok[DT];
     float rsum = 0.f;
+    if (chunks > 0) {
+        ys.store(yt, tid);
+        __syncthreads();
+    }
     for (int ci = 0; ci < chunks; ++ci) {
         const int c = live_end - 1 - ci;
-        const bool live = c * GC + tl < len, whole = (c + 1) * GC <= len;
-        const int rows = min(T - c * GC, GC);
         const int64_t tk0 = tok0 + (int64_t)c * GC;
-        const Gates gs = gate_sums(graw);
-        const float eh = lane_value(gs.h, 63), ef = lane_value(gs.f, 63);
-        float decay = pow2(eh + ef);
         for (int hy = 0; hy < w.G; ++hy) {
-            __syncthreads();                      // the last tile's reads are over
-            ys.store(yt, tid);
-            zs.store(zt, tid);
-            if (hy == 0) {
-                put_gates<true>(gh, gs, eh, ef, w.scale, 1.f, w.scale, wave, lane);
-#pragma unroll
-                for (int a = 0; a < ST::CW; ++a)
-#pragma unroll
-                    for (int e = 0; e < ST::EW; ++e)
-                        put4<E, D, NS>(stt, SB, 16 * ST::et(wave, e) + li, 16 * ST::ct(wave, a) + 4 * lg, S[a][e]);
-            }
-            __syncthreads();
             const bool last = hy + 1 == w.G;
+            const int at = in_loop<FRESH>(lane);
             fetch(last ? ci + 1 : ci, last ? 0 : hy + 1);
             if (hy == 0) {
-                fetch_x(ci + 1, kn, ktn, vn);
-                // from the state: dv = D^T k, dk = D v
+                fetch_x(ci + 1, w.k, kn);
+                fetch_x(ci + 1, w.v, vn);
+                // from the state: dk = D v
                 const float trw = rw[tl];
                 rsum = 0.f;
 #pragma unroll
                 for (int e = 0; e < DT; ++e) {
-                    f32x4 a = {0.f, 0.f, 0.f, 0.f}, c2 = a;
+                    f32x4 a = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                     for (int n = NS - 1; n >= 0; --n)
 #pragma unroll
-                        for (int kk = 0; kk < KD; ++kk) {
-                            if (n < NSV) a = mma(TL::rows(stt + n * SB, 16 * e, kk, lane), kf[kk], a);
-                            c2 = mma(TL::template cols<true>(stt + n * SB, kk, e, lane), vf[kk], c2);
-                        }
-                    ov[e] = a * trw;
-                    ok[e] = c2 * trw;
+                        for (int kk = 0; kk < KD; ++kk)
+                            a = mma(TL::template cols<true>(stt + n * SB, kk, e, at), vf[kk], a);   // rows by state_row(): e in row order
+                    ok[e] = a * trw;
                 }
 #pragma unroll
                 for (int kk = 0; kk < KD; ++kk) {
                     float u[8];
-                    widen(kt[kk], u);
+                    widen(kf[kk], u);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) rsum += u[j] * ok[2 * kk][j] + u[4 + j] * ok[2 * kk + 1][j];
                 }
             }
             const float th = gh[tl], tf = gh[GC + tl];
-            float p[GC / 16][4], m[GC / 16][4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) p[0][j] = m[0][j] = 0.f;
-#pragma unroll
-            for (int st = 1; st < GC / 16; ++st) {
-                f32x4 a = {0.f, 0.f, 0.f, 0.f}, c2 = a;
-#pragma unroll
-                for (int k = 0; k < KD; ++k) {
-                    a = mma(TL::rows(yt, 16 * st, k, lane), kf[k], a);
-                    c2 = mma(TL::rows(zt, 16 * st, k, lane), vf[k], c2);
-                }
-                const float rf = group_factor<true>(gh, th, tf, st, wave);
-                const f32x4 cs = *reinterpret_cast<const f32x4*>(cw + 16 * st + 4 * lg);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float wt = cs[j] * rf;
-                    p[st][j] = a[j] * wt;
-                    m[st][j] = c2[j] * wt;
-                    rsum += p[st][j] * c2[j];
-                }
-            }
+            float mown[4];
             {
-                f32x4 a = {0.f, 0.f, 0.f, 0.f}, c2 = a;
+                f32x4 a = {0.f, 0.f, 0.f, 0.f}, m = a;
 #pragma unroll
                 for (int k = 0; k < KD; ++k) {
-                    a = mma(TL::rows(yt, 16 * wave, k, lane), kf[k], a);
-                    c2 = mma(TL::rows(zt, 16 * wave, k, lane), vf[k], c2);
+                    a = mma(TL::rows(yt, 16 * wave, k, at), kf[k], a);
+                    m = mma(TL::rows(zt, 16 * wave, k, at), vf[k], m);
                 }
-                const f32x4 ow = own_weights<true>(gh, th, tf, w.scale, wave, lane);
+                own_pairs(m, own_weights<true>(gh, th, tf, w.scale, wave, lane), mown);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int t = 4 * lg + j;
-                    const float pv = t >= li ? a[j] * ow[j] : 0.f, mv = t >= li ? c2[j] * ow[j] : 0.f;
-                    rsum += t != li ? pv * c2[j] : 0.f;
-#pragma unroll
-                    for (int st = 0; st < GC / 16; ++st) {
-                        p[st][j] = st == wave ? pv : p[st][j];
-                        m[st][j] = st == wave ? mv : m[st][j];
-                    }
-                }
+                for (int j = 0; j < 4; ++j) rsum += 4 * lg + j != li ? mown[j] * a[j] : 0.f;
             }
 #pragma unroll
             for (int kk = 0; kk < GC / 32; ++kk) {
-                float pq[8], mq[8];
+                float mq[8];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    pq[j] = p[2 * kk][j];
-                    pq[4 + j] = p[2 * kk + 1][j];
-                    mq[j] = m[2 * kk][j];
-                    mq[4 + j] = m[2 * kk + 1][j];
+                for (int u = 0; u < 2; ++u) {
+                    const int st = 2 * kk + u;
+                    if (st == 0) {                // no row's other group
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) mq[j] = wave == 0 ? mown[j] : 0.f;
+                        continue;
+                    }
+                    f32x4 a = {0.f, 0.f, 0.f, 0.f}, m = a;
+#pragma unroll
+                    for (int k = 0; k < KD; ++k) {
+                        a = mma(TL::rows(yt, 16 * st, k, at), kf[k], a);
+                        m = mma(TL::rows(zt, 16 * st, k, at), vf[k], m);
+                    }
+                    const float rf = group_factor<true>(gh, th, tf, st, wave);
+                    const f32x4 cs = *reinterpret_cast<const f32x4*>(cw + 16 * st + 4 * lg);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float mv = m[j] * (cs[j] * rf);
+                        rsum += mv * a[j];
+                        mq[4 * u + j] = st == wave ? mown[j] : mv;
+                    }
                 }
-                Frag<E> pf[NP], mf[NP];
-                split<NP>(pq, pf);
+                Frag<E> mf[NP];
                 split<NP>(mq, mf);
 #pragma unroll
                 for (int e = 0; e < DT; ++e) {
-                    const Frag<E> z = TL::cols(zt, kk, e, lane), y = TL::cols(yt, kk, e, lane);
+                    const Frag<E> y = TL::template cols<true>(yt, kk, e, at);
 #pragma unroll
-                    for (int n = NP - 1; n >= 0; --n) {
-                        ov[e] = mma(z, pf[n], ov[e]);
-                        ok[e] = mma(y, mf[n], ok[e]);
-                    }
+                    for (int n = NP - 1; n >= 0; --n) ok[e] = mma(y, mf[n], ok[e]);
                 }
             }
+            __syncthreads();                      // the tiles' and the state's reads are over
+            ys.store(yt, tid);
             if (last) {
-                const __amdgpu_buffer_rsrc_t rv = rows_of<E>(w.dv, tk0, (int64_t)w.HK * D, hk * D, rows, D);
-                const __amdgpu_buffer_rsrc_t rk = rows_of<E>(w.dk, tk0, (int64_t)w.HK * D, hk * D, rows, D);
-                if (!whole) {
-#pragma unroll
-                    for (int e = 0; e < DT; ++e)
-                        if (!live) ov[e] = ok[e] = f32x4{0.f, 0.f, 0.f, 0.f};
-                }
-#pragma unroll
-                for (int e = 0; e < DT; ++e) {
-                    const int off = (tl * w.HK * D + 16 * e + 4 * lg) * ES;
-                    store_row4(rv, off, ov[e], E());
-                    store_row4(rk, off, ok[e], E());
-                }
+                store_rows(c, w.dk, ok);
                 float s = rsum + shfl_xor(rsum, 16);
                 s += shfl_xor(s, 32);             // all four lanes of a token store the same sum
-                __builtin_amdgcn_raw_buffer_store_b32(__float_as_int(live ? s : 0.f), rows_of<float>(w.r, tk0, w.HK, hk, rows, 1),
-                                                      tl * w.HK * 4, 0, 0);
+                __builtin_amdgcn_raw_buffer_store_b32(__float_as_int(c * GC + tl < len ? s : 0.f),
+                                                      rows_of<float>(w.r, tk0, w.HK, hk, min(T - c * GC, GC), 1), tl * w.HK * 4, 0, 0);
             }
-            if (keep || ci + 1 < chunks) update_state<E, D, D>(S, yt, zt, kw, decay, wave, lane);
-            decay = 1.f;
+            __syncthreads();
         }
 #pragma unroll
         for (int kk = 0; kk < KD; ++kk) {
             kf[kk] = kn[kk];
-            kt[kk] = ktn[kk];
             vf[kk] = vn[kk];
         }
     }
-    if (keep) store_state<D, D>(S, w.end + pair * D * D, D, 1, wave, lane);
 }
 
 // All three gradients in one launch: the walks for dq and for dk and dv (at D = 128 for dv
@@ -980,7 +1125,9 @@ struct Grads {
     Back kv;        // D <= 64
 };
 template <typename E, int D, int EB>
-__global__ void __launch_bounds__(THREADS, sizeof(E) == 2 || D == 32 ? 2 : 1) gated_grads(Grads w) {
+__global__ void __launch_bounds__((walk_threads<E, D>()), (!split_walk<E, D>() ? 2 : sizeof(E) == 2 || D == 32 ? 4 : 2))
+    gated_grads(Grads w) {
+    constexpr bool SPLIT = split_walk<E, D>();
     constexpr int NB = D / EB;
     constexpr int LDS = walk_lds<E, D, EB, true>();   // of D <= 64 the same for back()
     __shared__ __attribute__((aligned(16))) char lds[LDS];
@@ -988,12 +1135,12 @@ __global__ void __launch_bounds__(THREADS, sizeof(E) == 2 || D == 32 ? 2 : 1) ga
     if constexpr (NB == 1) {
         static_assert(D == EB, "back() has all columns");
         if ((n & 1) == 0) back<E, D>(w.kv, n >> 1, lds);
-        else walk<E, D, EB, false, true>(w.q, n >> 1, lds);
+        else walk<E, D, EB, false, true, true>(w.q, n >> 1, lds);
     } else {
         const int role = (n / NB) % 3, id = n / (3 * NB) * NB + n % NB;
-        if (role == 0) walk<E, D, EB, true, true>(w.k, id, lds);
-        else if (role == 1) walk<E, D, EB, false, true>(w.q, id, lds);
-        else walk<E, D, EB, true, false>(w.v, id, lds);
+        if (role == 0) walk<E, D, EB, true, true, SPLIT>(w.k, id, lds);
+        else if (role == 1) walk<E, D, EB, false, true, SPLIT>(w.q, id, lds);
+        else walk<E, D, EB, true, false, SPLIT>(w.v, id, lds);
     }
 }
 
@@ -1162,8 +1309,9 @@ __global__ void __launch_bounds__(64 * JOIN_WAVES) gated_join(float* fst, const 
 struct GateGrad {
     const float* rq;
     const float* rk;
-    const float* fst;
-    const float* rst;
+    const float* fst;    // state after each segment
+    int64_t fst_pair;
+    const float* rst;    // its gradient, or nullptr (zero)
     const float* g;
     const int32_t* lens;
     float* dg;
@@ -1201,10 +1349,10 @@ __global__ void __launch_bounds__(THREADS) gated_gate_grad(GateGrad w) {
             }
         }
     }
-    const float* S = w.fst + (pair * (w.nseg + 1) + seg + 1) * w.DD;
+    const float* S = w.fst + pair * w.fst_pair + (int64_t)seg * w.DD;
     const float* R = w.rst + (pair * w.nseg + seg) * w.DD;
     double cross = 0.0;
-    for (int i = tid * 4; i < w.DD; i += THREADS * 4) {
+    for (int i = tid * 4; w.rst && i < w.DD; i += THREADS * 4) {
         const f32x4 s = load4(S + i), r = load4(R + i);
 #pragma unroll
         for (int j = 0; j < 4; ++j) cross += (double)s[j] * (double)r[j];
@@ -1336,7 +1484,7 @@ __global__ void __launch_bounds__(THREADS) gated_step(GatedStep w) {
 // ---------------------------------------------------------------- launches
 template <typename E, int D>
 hipError_t launch_local(const Local& w, hipStream_t stream) {
-    constexpr int EB = D < 64 ? D : 64;
+    constexpr int EB = gated_value_block(D);
     const int64_t n = (int64_t)w.B * w.HK * w.nseg * w.roles * (D / EB);
     gated_local<E, D, EB><<<dim3((unsigned)n), THREADS, 0, stream>>>(w);
     return hipGetLastError();
@@ -1393,8 +1541,8 @@ hipError_t forward(const GatedForward& f) {
     w.B = p.B; w.T = p.T; w.HK = p.HK; w.nx = p.H / p.HK; w.ny = 1; w.nseg = p.nseg; w.seg_chunks = p.seg_chunks;
     w.pair_scale = w.row_scale = p.scale;
     w.key_scale = 1.f;
-    constexpr int EB = D < 64 ? D : 64;
-    gated_walk<E, D, EB><<<dim3((unsigned)((int64_t)p.B * p.HK * p.nseg * (D / EB))), THREADS, 0, p.stream>>>(w);
+    constexpr int EB = gated_value_block(D);
+    gated_walk<E, D, EB><<<dim3((unsigned)((int64_t)p.B * p.HK * p.nseg * (D / EB))), (walk_threads<E, D>()), 0, p.stream>>>(w);
     return hipGetLastError();
 }
 
@@ -1404,27 +1552,29 @@ hipError_t backward(const GatedBackward& f) {
     const int G = p.H / p.HK, DD = D * D;
     const int64_t hs = (int64_t)p.H * D;
     hipError_t err;
-    Local l = {};
-    l.roles = 2;
-    l.y[0] = {p.k, p.ks};
-    l.z[0] = {p.v, p.vs};
-    l.y[1] = {p.q, p.qs};
-    l.z[1] = {f.dout, hs};
-    l.ny[0] = 1;
-    l.ny[1] = G;
-    l.st[0] = f.fst;
-    l.st[1] = f.rst;
-    l.pair[0] = (int64_t)(p.nseg + 1) * DD;
-    l.pair[1] = (int64_t)p.nseg * DD;
-    l.first[0] = DD;
-    l.key_scale[0] = 1.f;
-    l.key_scale[1] = p.scale;
-    l.dec = f.fdec;
-    l.g = p.g;
-    l.lens = p.lens;
-    l.B = p.B; l.T = p.T; l.HK = p.HK; l.nseg = p.nseg; l.seg_chunks = p.seg_chunks;
-    if ((err = launch_local<E, D>(l, p.stream)) != hipSuccess) return err;
-    if ((err = launch_join(f.fst, p.s0, f.rst, f.ds1, f.fdec, p.B * p.HK, p.nseg, DD, p.stream)) != hipSuccess) return err;
+    if (p.nseg > 1) {
+        Local l = {};
+        l.roles = 2;
+        l.y[0] = {p.k, p.ks};
+        l.z[0] = {p.v, p.vs};
+        l.y[1] = {p.q, p.qs};
+        l.z[1] = {f.dout, hs};
+        l.ny[0] = 1;
+        l.ny[1] = G;
+        l.st[0] = f.fst;
+        l.st[1] = f.rst;
+        l.pair[0] = (int64_t)(p.nseg + 1) * DD;
+        l.pair[1] = (int64_t)p.nseg * DD;
+        l.first[0] = DD;
+        l.key_scale[0] = 1.f;
+        l.key_scale[1] = p.scale;
+        l.dec = f.fdec;
+        l.g = p.g;
+        l.lens = p.lens;
+        l.B = p.B; l.T = p.T; l.HK = p.HK; l.nseg = p.nseg; l.seg_chunks = p.seg_chunks;
+        if ((err = launch_local<E, D>(l, p.stream)) != hipSuccess) return err;
+        if ((err = launch_join(f.fst, p.s0, f.rst, f.ds1, f.fdec, p.B * p.HK, p.nseg, DD, p.stream)) != hipSuccess) return err;
+    }
 
     Grads gr = {};
     Walk& w = gr.q;       // dq and q . dq
@@ -1438,8 +1588,10 @@ hipError_t backward(const GatedBackward& f) {
     w.x2 = {p.q, p.qs};
     w.out = f.dq;
     w.r = f.rq;
-    w.start = f.fst;
-    w.start_pair = (int64_t)(p.nseg + 1) * DD;
+    w.start = p.nseg > 1 ? f.fst : p.s0;
+    w.start_pair = p.nseg > 1 ? (int64_t)(p.nseg + 1) * DD : DD;
+    // one segment: the state after it, for its product with its gradient
+    w.end = p.nseg > 1 || !f.ds1 ? nullptr : f.fst;
     w.sc = 1; w.se = D;
     w.nx = G; w.ny = 1;
     w.pair_scale = w.row_scale = p.scale;
@@ -1455,7 +1607,7 @@ hipError_t backward(const GatedBackward& f) {
         k.r = f.rk;
         k.g = p.g;
         k.lens = p.lens;
-        k.start = f.rst;
+        k.start = p.nseg > 1 ? f.rst : f.ds1;
         k.end = f.ds0;
         k.B = p.B; k.T = p.T; k.HK = p.HK; k.G = G; k.nseg = p.nseg; k.seg_chunks = p.seg_chunks;
         k.scale = p.scale;
@@ -1468,7 +1620,7 @@ hipError_t backward(const GatedBackward& f) {
         v.x2 = {nullptr, 0};
         v.out = f.dv;
         v.r = nullptr;
-        v.start = f.rst;
+        v.start = p.nseg > 1 ? f.rst : f.ds1;
         v.start_pair = (int64_t)p.nseg * DD;
         v.end = f.ds0;
         v.sc = D; v.se = 1;
@@ -1486,13 +1638,19 @@ hipError_t backward(const GatedBackward& f) {
         k.end = nullptr;
         k.sc = 1; k.se = D;
     }
-    constexpr int EB = D < 64 ? D : 64;
-    gated_grads<E, D, EB><<<dim3((unsigned)((int64_t)p.B * p.HK * p.nseg * (D / EB) * (D <= 64 ? 2 : 3))), THREADS, 0,
+    constexpr int EB = gated_value_block(D);
+    gated_grads<E, D, EB><<<dim3((unsigned)((int64_t)p.B * p.HK * p.nseg * (D / EB) * (D <= 64 ? 2 : 3))),
+                            (walk_threads<E, D>()), 0,
                             p.stream>>>(gr);
     if ((err = hipGetLastError()) != hipSuccess) return err;
 
     GateGrad d;
-    d.rq = f.rq; d.rk = f.rk; d.fst = f.fst; d.rst = f.rst; d.g = p.g; d.lens = p.lens; d.dg = f.dg;
+    d.rq = f.rq; d.rk = f.rk; d.g = p.g;
+    // one segment: <S, dS> of the final state, or none
+    d.fst = p.nseg > 1 ? f.fst + DD : f.fst;
+    d.fst_pair = p.nseg > 1 ? (int64_t)(p.nseg + 1) * DD : DD;
+    d.rst = p.nseg > 1 ? f.rst : f.ds1;
+    d.lens = p.lens; d.dg = f.dg;
     d.B = p.B; d.T = p.T; d.HK = p.HK; d.nx = G; d.nb = gated_value_blocks(D); d.nseg = p.nseg;
     d.seg_chunks = p.seg_chunks; d.DD = DD;
     gated_gate_grad<<<dim3((unsigned)((int64_t)p.B * p.HK * p.nseg)), THREADS, 0, p.stream>>>(d);
@@ -1501,7 +1659,7 @@ hipError_t backward(const GatedBackward& f) {
 
 template <typename E, int D>
 hipError_t step(const GatedStep& s) {
-    constexpr int EB = D < 64 ? D : 64;
+    constexpr int EB = gated_value_block(D);
     gated_step<E, D, EB><<<dim3((unsigned)((int64_t)s.B * s.HK * (D / EB))), THREADS, 0, s.stream>>>(s);
     return hipGetLastError();
 }

@@ -915,12 +915,15 @@ mhla_status check_seq(const mhla_seq* q, Seq* s, bool groups) {
     return MHLA_OK;
 }
 
-// Segments of a sequence: workgroups walk them side by side, at most as many as the compute
-// units hold at once (256 of them: the plan fixes the workspace, so it goes by the problem
-// alone).  A few more would run as a second round, as long as the first: dit-s2-256x256 as
-// one sequence, forwards 81 us with 768 walks, 96 with 1024, 93 with 512; backwards 234 us
-// with 512, 254 with 1024.  Short sequences are split down to single chunks, which shortens
-// the longest walk (4 x 1000 tokens, head_dim 128: 31 us against 48 with four chunks a walk).
+// Segments of a sequence: workgroups walk them side by side, for one more pass over the keys
+// and values and a state a segment written and read.  Forwards a sequence is split where
+// there is less than a walk for each of 256 compute units (16 x 4096 tokens, 16 heads of 64:
+// one segment 144 us, two 212), into about as many walks as run at once (a few more would run
+// as a second round, as long as the first), and not at all up to FEW chunks, which one walk
+// goes through in the time of the two launches that splitting adds (4 heads, one segment and
+// split: 512 tokens of 64 bf16 forwards 16.3 and 19.1 us; 256 tokens of 128 bf16 forwards 15.5
+// and 19.0, backwards 30.4 and 32.5; 128 tokens of 128 fp32 forwards 19.1 and 20.4).  The plan
+// fixes the workspace, so it goes by the problem alone.
 // Backwards, segments of at most MOST chunks: the gates' gradients start anew from <S, dS>
 // at each segment's end.
 struct GatedPlan {
@@ -931,7 +934,10 @@ GatedPlan gated_plan(const Seq& s, bool backward) {
     constexpr int64_t CUS = 256, MOST = mhla::GATED_MAX_CHUNKS;
     const int64_t C = mhla::GATED_CHUNK, chunks = s.T > 0 ? (s.T + C - 1) / C : 1;
     const int64_t walks = s.B * s.HK * mhla::gated_value_blocks((int)s.D);
-    int64_t n = CUS * mhla::gated_walks_per_cu(s.esz == 2, (int)s.D, backward) / walks;
+    const bool bf16 = s.esz == 2;
+    const int64_t few = !bf16 && s.D == 128 ? 2 : bf16 && s.D <= 64 && !backward ? 8 : 4;
+    int64_t n = CUS * mhla::gated_walks_per_cu(bf16, (int)s.D, backward) / walks;
+    if ((!backward && walks >= CUS) || chunks <= few) n = 1;
     if (n > chunks) n = chunks;
     if (backward && n < (chunks + MOST - 1) / MOST) n = (chunks + MOST - 1) / MOST;
     if (n < 1) n = 1;
@@ -940,15 +946,16 @@ GatedPlan gated_plan(const Seq& s, bool backward) {
     p.nseg = (int)((chunks + p.seg_chunks - 1) / p.seg_chunks);
     const size_t pairs = (size_t)(s.B * s.HK), state = (size_t)(s.D * s.D) * 4;
     const size_t nb = (size_t)mhla::gated_value_blocks((int)s.D);
+    const size_t split = p.nseg > 1 ? 1 : 0;
     p.fst = 0;
-    p.dec = p.fst + align_up(pairs * (size_t)(p.nseg + 1) * state);
-    p.rst = p.dec + align_up(pairs * (size_t)p.nseg * 4);
+    p.dec = p.fst + align_up(pairs * (split ? (size_t)(p.nseg + 1) : (size_t)backward) * state);
+    p.rst = p.dec + split * align_up(pairs * (size_t)p.nseg * 4);
     if (!backward) {
         p.rq = p.rk = p.rst;
-        p.total = p.nseg > 1 ? p.rst : 0;
+        p.total = split ? p.rst : 0;
         return p;
     }
-    p.rq = p.rst + align_up(pairs * (size_t)p.nseg * state);
+    p.rq = p.rst + split * align_up(pairs * (size_t)p.nseg * state);
     p.rk = p.rq + align_up(nb * (size_t)(s.tokens() * s.H) * 4);
     p.total = p.rk + align_up(nb * (size_t)(s.tokens() * s.HK) * 4);
     return p;
