@@ -442,6 +442,14 @@ __device__ __forceinline__ int in_loop(int lane) {
 }
 
 // ---------------------------------------------------------------- the walk
+// Whether groups of 16 tokens that none of a wave's rows sees are left out.  Worth its branches
+// at D = 128 in bf16, where the matrix cores have most to do (forwards, 16 x 4096 tokens, 8
+// heads: 273 -> 233 us; backwards 2 x 4097 tokens, 12 heads over 4: 164 -> 160); at D = 64 it
+// costs as much as it saves (16 x 4096, 16 heads: 144 -> 152), and fp32 loses a workgroup of a
+// compute unit to its registers (2 x 4096, 70 heads of 32: 122 -> 126).
+template <typename E, int D>
+constexpr bool SKIP_UNSEEN = sizeof(E) == 2 && D == 128;
+
 // One role: [B, T, heads, D] with a token stride.
 struct Role {
     const void* p;
@@ -510,6 +518,7 @@ __device__ __forceinline__ void walk(const Walk& w, int id, char* lds) {
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) & 3;         // in its group
     const int tid = threadIdx.x & (THREADS - 1), lane = tid & 63, li = lane & 15, lg = lane >> 4;
     constexpr int NB = D / EB;
+    const int number = id;
     const int eb = id % NB;
     id /= NB;
     const int hk = id % w.HK;
@@ -604,7 +613,10 @@ __device__ __forceinline__ void walk(const Walk& w, int id, char* lds) {
     // ---- the rows' part
     const int hx_all = w.HK * w.nx;
     float* const rout = DOT ? w.r + (int64_t)eb * w.B * T * hx_all : nullptr;
-    const int tl = 16 * wave + li;                        // this lane's token in a chunk
+    // which wave has which rows turns with the workgroup, so that the long ones spread over the SIMDs
+    constexpr bool SKIP = SKIP_UNSEEN<E, D>;
+    const int own_group = SKIP ? (wave + number) & 3 : wave;
+    const int tl = 16 * own_group + li;                   // this lane's token in a chunk
     Frag<E> xf[KD], x2f[DOT ? KE : 1];
     auto fetch_x = [&](int ci, int hx, Frag<E> (&x)[KD], Frag<E> (&x2)[DOT ? KE : 1]) {
         const int c = first + dir * ci;
@@ -638,126 +650,127 @@ __device__ __forceinline__ void walk(const Walk& w, int id, char* lds) {
 
     f32x4 o[ET];
     float rsum = 0.f;
-            auto store_rows = [&](int ci, int hx) {
+    auto store_rows = [&](int ci, int hx) {
         const int c = first + dir * ci;
         const bool live = c * GC + tl < len, whole = (c + 1) * GC <= len;
         const int rows = min(T - c * GC, GC);
         const int64_t tk0 = tok0 + (int64_t)c * GC;
-                const int h = hk * nx + hx;
-                const __amdgpu_buffer_rsrc_t ro = rows_of<E>(w.out, tk0, (int64_t)hx_all * D, h * D + eb * EB, rows, EB);
-                if (!whole) {
-    #pragma unroll
-                    for (int e = 0; e < ET; ++e)
-                        if (!live) o[e] = f32x4{0.f, 0.f, 0.f, 0.f};
-                }
-    #pragma unroll
-                for (int k = 0; k < KE; ++k)
-                    store_row8(ro, (tl * hx_all * D + 32 * k + 8 * lg) * ES, o[2 * k], o[2 * k + 1], E());
-                if constexpr (DOT) {
-                    float s = rsum + shfl_xor(rsum, 16);
-                    s += shfl_xor(s, 32);             // all four lanes of a token store the same sum
-                    const __amdgpu_buffer_rsrc_t rr = rows_of<float>(rout, tk0, hx_all, h, rows, 1);
-                    __builtin_amdgcn_raw_buffer_store_b32(__float_as_int(live ? s : 0.f), rr, tl * hx_all * 4, 0, 0);
-                }
-            };
+        const int h = hk * nx + hx;
+        const __amdgpu_buffer_rsrc_t ro = rows_of<E>(w.out, tk0, (int64_t)hx_all * D, h * D + eb * EB, rows, EB);
+        if (!whole) {
+#pragma unroll
+            for (int e = 0; e < ET; ++e)
+                if (!live) o[e] = f32x4{0.f, 0.f, 0.f, 0.f};
+        }
+#pragma unroll
+        for (int k = 0; k < KE; ++k)
+            store_row8(ro, (tl * hx_all * D + 32 * k + 8 * lg) * ES, o[2 * k], o[2 * k + 1], E());
+        if constexpr (DOT) {
+            float s = rsum + shfl_xor(rsum, 16);
+            s += shfl_xor(s, 32);             // all four lanes of a token store the same sum
+            const __amdgpu_buffer_rsrc_t rr = rows_of<float>(rout, tk0, hx_all, h, rows, 1);
+            __builtin_amdgcn_raw_buffer_store_b32(__float_as_int(live ? s : 0.f), rr, tl * hx_all * 4, 0, 0);
+        }
+    };
     // the outputs of the tiles in LDS, all heads of X; all but the last head's are stored
     auto compute_rows = [&](int ci, int hy) {
         const bool last_y = hy + 1 == ny;
-                    const float th = gh[tl], tf = gh[GC + tl], trw = rw[tl];
-                    for (int hx = 0; hx < nx; ++hx) {
-                        const bool last_x = hx + 1 == nx;
-                        const int at = in_loop<FRESH>(lane);
-                        Frag<E> xn[KD], x2n[DOT ? KE : 1];
-                        if (!REV || last_y) fetch_x(last_x ? ci + 1 : ci, last_x ? 0 : hx + 1, xn, x2n);
-                        if (!REV || hy == 0) {
-                            // from the state: o = S^T x
-                            rsum = 0.f;
-        #pragma unroll
-                            for (int e = 0; e < ET; ++e) {
-                                f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-        #pragma unroll
-                                for (int n = NS - 1; n >= 0; --n)
-        #pragma unroll
-                                    for (int kk = 0; kk < KD; ++kk)
-                                        acc = mma(TY::rows(stt + n * SB, 16 * e, kk, at), xf[kk], acc);
-                                o[e] = acc * trw;
-                            }
-                            if constexpr (DOT) {
-        #pragma unroll
-                                for (int kk = 0; kk < KE; ++kk) {
-                                    float u[8];
-                                    widen(x2f[kk], u);
-        #pragma unroll
-                                    for (int j = 0; j < 4; ++j) rsum += u[j] * o[2 * kk][j] + u[4 + j] * o[2 * kk + 1][j];
-                                }
-                            }
-                        }
-                        // the chunk's tokens s, 32 at a time: the row's own group of 16 and the groups that come before
-                        // (backwards: after) it, the others' weight being 0
-                        float own[4];
-                        {
-                            f32x4 acc = {0.f, 0.f, 0.f, 0.f}, m = {0.f, 0.f, 0.f, 0.f};
-        #pragma unroll
-                            for (int k = 0; k < KD; ++k) acc = mma(TY::rows(yt, 16 * wave, k, at), xf[k], acc);
-                            if constexpr (DOT) {
-        #pragma unroll
-                                for (int k = 0; k < KE; ++k) m = mma(TZ::rows(zt, 16 * wave, k, at), x2f[k], m);
-                            }
-                            const f32x4 ow = own_weights<REV>(gh, th, tf, w.pair_scale, wave, lane);
-        #pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                const int s = 4 * lg + j;
-                                const float v = acc[j] * ow[j];
-                                own[j] = (REV ? s >= li : s <= li) ? v : 0.f;
-                                if constexpr (DOT) rsum += s != li ? own[j] * m[j] : 0.f;
-                            }
-                        }
-        #pragma unroll
-                        for (int kk = 0; kk < GC / 32; ++kk) {
-                            float q[8];
-        #pragma unroll
-                            for (int u = 0; u < 2; ++u) {
-                                const int st = 2 * kk + u;
-                                if (st == (REV ? 0 : GC / 16 - 1)) {      // no row's other group
-        #pragma unroll
-                                    for (int j = 0; j < 4; ++j) q[4 * u + j] = st == wave ? own[j] : 0.f;
-                                    continue;
-                                }
-                                f32x4 acc = {0.f, 0.f, 0.f, 0.f}, m = {0.f, 0.f, 0.f, 0.f};
-        #pragma unroll
-                                for (int k = 0; k < KD; ++k) acc = mma(TY::rows(yt, 16 * st, k, at), xf[k], acc);
-                                if constexpr (DOT) {
-        #pragma unroll
-                                    for (int k = 0; k < KE; ++k) m = mma(TZ::rows(zt, 16 * st, k, at), x2f[k], m);
-                                }
-                                const float rf = group_factor<REV>(gh, th, tf, st, wave);
-                                const f32x4 cs = *reinterpret_cast<const f32x4*>(cw + 16 * st + 4 * lg);
-        #pragma unroll
-                                for (int j = 0; j < 4; ++j) {
-                                    const float v = acc[j] * (cs[j] * rf);
-                                    if constexpr (DOT) rsum += v * m[j];
-                                    q[4 * u + j] = st == wave ? own[j] : v;
-                                }
-                            }
-                            Frag<E> pf[NP];
-                            split<NP>(q, pf);
-        #pragma unroll
-                            for (int e = 0; e < ET; ++e) {
-                                const Frag<E> z = TZ::template cols<true>(zt, kk, e, at);
-        #pragma unroll
-                                for (int n = NP - 1; n >= 0; --n) o[e] = mma(z, pf[n], o[e]);
-                            }
-                        }
-                        if (!REV || last_y) {
-        #pragma unroll
-                            for (int kk = 0; kk < KD; ++kk) xf[kk] = xn[kk];
-                            if constexpr (DOT) {
-        #pragma unroll
-                                for (int kk = 0; kk < KE; ++kk) x2f[kk] = x2n[kk];
-                            }
-                        }
-                        if (!last_x) store_rows(ci, hx);
+        const float th = gh[tl], tf = gh[GC + tl], trw = rw[tl];
+        for (int hx = 0; hx < nx; ++hx) {
+            const bool last_x = hx + 1 == nx;
+            const int at = in_loop<FRESH>(lane);
+            Frag<E> xn[KD], x2n[DOT ? KE : 1];
+            if (!REV || last_y) fetch_x(last_x ? ci + 1 : ci, last_x ? 0 : hx + 1, xn, x2n);
+            if (!REV || hy == 0) {
+                // from the state: o = S^T x
+                rsum = 0.f;
+#pragma unroll
+                for (int e = 0; e < ET; ++e) {
+                    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int n = NS - 1; n >= 0; --n)
+#pragma unroll
+                        for (int kk = 0; kk < KD; ++kk)
+                            acc = mma(TY::rows(stt + n * SB, 16 * e, kk, at), xf[kk], acc);
+                    o[e] = acc * trw;
+                }
+                if constexpr (DOT) {
+#pragma unroll
+                    for (int kk = 0; kk < KE; ++kk) {
+                        float u[8];
+                        widen(x2f[kk], u);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) rsum += u[j] * o[2 * kk][j] + u[4 + j] * o[2 * kk + 1][j];
                     }
+                }
+            }
+            // the chunk's tokens s, 32 at a time: the row's own group of 16 and the groups that come before
+            // (backwards: after) it, the others' weight being 0
+            float own[4];
+            {
+                f32x4 acc = {0.f, 0.f, 0.f, 0.f}, m = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int k = 0; k < KD; ++k) acc = mma(TY::rows(yt, 16 * own_group, k, at), xf[k], acc);
+                if constexpr (DOT) {
+#pragma unroll
+                    for (int k = 0; k < KE; ++k) m = mma(TZ::rows(zt, 16 * own_group, k, at), x2f[k], m);
+                }
+                const f32x4 ow = own_weights<REV>(gh, th, tf, w.pair_scale, own_group, lane);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int s = 4 * lg + j;
+                    const float v = acc[j] * ow[j];
+                    own[j] = (REV ? s >= li : s <= li) ? v : 0.f;
+                    if constexpr (DOT) rsum += s != li ? own[j] * m[j] : 0.f;
+                }
+            }
+#pragma unroll
+            for (int kk = 0; kk < GC / 32; ++kk) {
+                if (SKIP && (REV ? 2 * kk + 1 < own_group : 2 * kk > own_group)) continue;
+                float q[8];
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const int st = 2 * kk + u;
+                    if (st == (REV ? 0 : GC / 16 - 1) || (SKIP && (REV ? st <= own_group : st >= own_group))) {   // no other group's
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) q[4 * u + j] = st == own_group ? own[j] : 0.f;
+                        continue;
+                    }
+                    f32x4 acc = {0.f, 0.f, 0.f, 0.f}, m = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int k = 0; k < KD; ++k) acc = mma(TY::rows(yt, 16 * st, k, at), xf[k], acc);
+                    if constexpr (DOT) {
+#pragma unroll
+                        for (int k = 0; k < KE; ++k) m = mma(TZ::rows(zt, 16 * st, k, at), x2f[k], m);
+                    }
+                    const float rf = group_factor<REV>(gh, th, tf, st, own_group);
+                    const f32x4 cs = *reinterpret_cast<const f32x4*>(cw + 16 * st + 4 * lg);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float v = acc[j] * (cs[j] * rf);
+                        if constexpr (DOT) rsum += v * m[j];
+                        q[4 * u + j] = st == own_group ? own[j] : v;
+                    }
+                }
+                Frag<E> pf[NP];
+                split<NP>(q, pf);
+#pragma unroll
+                for (int e = 0; e < ET; ++e) {
+                    const Frag<E> z = TZ::template cols<true>(zt, kk, e, at);
+#pragma unroll
+                    for (int n = NP - 1; n >= 0; --n) o[e] = mma(z, pf[n], o[e]);
+                }
+            }
+            if (!REV || last_y) {
+#pragma unroll
+                for (int kk = 0; kk < KD; ++kk) xf[kk] = xn[kk];
+                if constexpr (DOT) {
+#pragma unroll
+                    for (int kk = 0; kk < KE; ++kk) x2f[kk] = x2n[kk];
+                }
+            }
+            if (!last_x) store_rows(ci, hx);
+        }
     };
     if constexpr (SPLIT) {
         if (chunks > 0) __syncthreads();
@@ -959,9 +972,9 @@ __device__ __forceinline__ void back(const Back& w, int id, char* lds) {
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
                         const int st = 2 * kk + u;
-                        if (st == 0) {            // no row's other group
+                        if (st == 0) {   // no other group's
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) pq[j] = wave == 0 ? pown[j] : 0.f;
+                            for (int j = 0; j < 4; ++j) pq[4 * u + j] = st == wave ? pown[j] : 0.f;
                             continue;
                         }
                         f32x4 a = {0.f, 0.f, 0.f, 0.f};
@@ -1069,9 +1082,9 @@ __device__ __forceinline__ void back(const Back& w, int id, char* lds) {
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     const int st = 2 * kk + u;
-                    if (st == 0) {                // no row's other group
+                    if (st == 0) {   // no other group's
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) mq[j] = wave == 0 ? mown[j] : 0.f;
+                        for (int j = 0; j < 4; ++j) mq[4 * u + j] = st == wave ? mown[j] : 0.f;
                         continue;
                     }
                     f32x4 a = {0.f, 0.f, 0.f, 0.f}, m = a;
