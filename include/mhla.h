@@ -544,10 +544,10 @@ mhla_status mhla_gated_forward(const void* q, const void* k, const void* v, cons
  *   dq_t = scale * S_t dout_t,  dk_t = D_t v_t,  dv_t = D_t^T k_t
  *   dg_t = exp(g_t) <S_{t-1}, D_t>,  dstate = exp(g_1) D_1
  *
- * dq, dk, dv in the problem's dtype, contiguous; dg fp32 (zero where exp(g) is
- * zero in fp32); dstate: the initial state's gradient or NULL; it may be
- * dstate_out itself.  The states are recomputed.  Other arguments and rules as
- * for mhla_gated_forward. */
+ * dq, dk, dv in the problem's dtype, contiguous; dg fp32: zero where exp(g) is
+ * zero in fp32, and its sums start again there; dstate: the initial state's gradient or NULL.  No output may
+ * overlap an input (dstate not dstate_out either) or another output.  The
+ * states are recomputed.  Other arguments and rules as for mhla_gated_forward. */
 mhla_status mhla_gated_backward(const void* q, const void* k, const void* v, const float* g, const int32_t* lens,
                                 const float* state, const void* dout, const float* dstate_out, const mhla_seq* seq,
                                 void* dq, void* dk, void* dv, float* dg, float* dstate, void* ws, size_t ws_bytes,

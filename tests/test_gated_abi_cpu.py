@@ -74,7 +74,7 @@ def test_forward_refusals(kw, code):
     ({"do": None}, INV), ({"dq": None}, INV), ({"dk": None}, INV), ({"dv": None}, INV), ({"dg": None}, INV),
     ({"do": P(7, 8)}, MIS), ({"ds1": P(8, 4)}, MIS), ({"ds0": P(13, 8)}, MIS), ({"dg": P(12, 2)}, MIS),
     ({"dq": P(7)}, INV), ({"dk": P(2)}, INV), ({"dv": P(10)}, INV), ({"dg": P(4)}, INV), ({"ds0": P(6)}, INV),
-    ({"ds0": P(8, 16)}, INV), ({"ws": P(9)}, INV), ({"ws": P(7)}, INV), ({"n": 1000}, INV), ({"ws": P(14, 4)}, MIS),
+    ({"ds0": P(8, 16)}, INV), ({"ds0": P(8)}, INV), ({"ws": P(9)}, INV), ({"ws": P(7)}, INV), ({"n": 1000}, INV), ({"ws": P(14, 4)}, MIS),
 ])
 def test_backward_refusals(kw, code):
     assert bwd(**kw) == code

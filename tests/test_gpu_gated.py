@@ -87,6 +87,7 @@ SHAPES = [
     (1, 1, 1, 1, 32, BF), (2, 1, 4, 2, 64, F32), (1, 63, 2, 2, 64, BF), (2, 64, 3, 1, 32, F32),
     (1, 65, 2, 1, 128, BF), (1, 130, 2, 2, 128, F32), (3, 200, 6, 2, 64, BF), (2, 321, 4, 4, 32, BF),
     (1, 577, 2, 2, 64, F32), (2, 260, 4, 1, 128, BF), (1, 700, 3, 3, 32, F32), (1, 1300, 1, 1, 64, BF),
+    (32, 200, 8, 8, 32, BF), (1, 900, 6, 2, 128, F32), (2, 1100, 3, 1, 128, BF), (1, 128, 3, 3, 128, F32),
 ]
 
 
@@ -243,6 +244,79 @@ def test_repeats_give_the_same_bits_on_another_stream_and_workspace():
     assert mh.mhla_gated_forward(q, k, v, dev(x["g"]), seq, out, None, st, st) == mh.MHLA_OK
     torch.cuda.synchronize()
     assert torch.equal(a, out) and torch.equal(Sa, st)
+
+
+def test_packed_gradients_do_not_see_each_other():
+    """Gates' gradients of packed sequences, one of them with values 10^6 times as large: each sequence's are
+    those it gives alone, within its own sums' tolerance."""
+    H, Hk, d = 2, 2, 64
+    parts = [1, 70, 64, 130, 3, 90]
+    x = inputs(14, F32, 1, sum(parts), H, Hk, d, False)
+    t0 = 0
+    for i, n in enumerate(parts):
+        x["g"][0, t0] = -np.inf
+        if i == 3:
+            x["q"][:, t0:t0 + n] *= 2.0 ** 20
+            x["v"][:, t0:t0 + n] *= 2.0 ** 20
+        t0 += n
+    q, k, v, g, do = (dev(x[n]) for n in ("q", "k", "v", "g", "do"))
+    dg = mh.gated_backward(q, k, v, g, do, 1.0)[3]
+    torch.cuda.synchronize()
+    t0 = 0
+    for n in parts:
+        y = {m: a if a is None else a[:, t0:t0 + n] for m, a in x.items()}
+        ref = og.gated_backward(y["q"], y["k"], y["v"], y["g"], y["do"], 1.0)[3]
+        check_gate_gradient(dg[:, t0:t0 + n], ref, y, 1.0, d, n)
+        t0 += n
+
+
+def test_two_streams_at_once():
+    """Two calls with workspaces of their own, running side by side many times, give what each gives alone."""
+    xs = [inputs(30 + i, BF, 1, 3000, 2, 2, 64) for i in range(2)]
+    alone = []
+    for x in xs:
+        (q, k, v, _, s0), a, Sa = run_forward(x, BF, 0.3)
+        g, do, ds1 = dev(x["g"]), dev(x["do"], BF), dev(x["ds1"])
+        alone.append(((q, k, v, g, do, s0, ds1), (a, Sa, *mh.gated_backward(q, k, v, g, do, 0.3, s0, ds1))))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in xs]
+    got = [None, None]
+    for _ in range(5):
+        for i, s in enumerate(streams):
+            q, k, v, g, do, s0, ds1 = alone[i][0]
+            with torch.cuda.stream(s):
+                out, S = mh.gated_forward(q, k, v, g, 0.3, s0, want_state=True)
+                got[i] = (out, S, *mh.gated_backward(q, k, v, g, do, 0.3, s0, ds1))
+    torch.cuda.synchronize()
+    for (_, want), have in zip(alone, got):
+        for a, b in zip(want, have):
+            assert torch.equal(a, b)
+
+
+def test_offsets_past_32_bits():
+    """Tensors of more than 2^31 values: the last tokens, behind a gate of 0, give what they give alone."""
+    H, d, T, tail = 64, 64, 560000, 200
+    assert T * H * d > 1 << 31
+    gen = torch.Generator(device="cuda").manual_seed(0)
+    small = [torch.randn(1, tail, H, d, generator=gen, device="cuda").to(BF) for _ in range(4)]
+    gs = -0.1 * torch.rand(1, tail, H, generator=gen, device="cuda")
+    gs[:, 0] = -float("inf")
+    q, k, v, do = (torch.zeros(1, T, H, d, dtype=BF, device="cuda") for _ in range(4))
+    g = torch.zeros(1, T, H, device="cuda")
+    for a, b in zip((q, k, v, do, g), (*small, gs)):
+        a[:, T - tail:] = b
+    say(f"  [gpu] gated forward and backward over {q.numel()} values")
+    # the short call starts at a chunk of its own, the long one inside a chunk: other sums of the same terms
+    want = (mh.gated_forward(*small[:3], gs, 0.1), *mh.gated_backward(*small[:3], gs, small[3], 0.1)[:4])
+    out = mh.gated_forward(q, k, v, g, 0.1)
+    grads = mh.gated_backward(q, k, v, g, do, 0.1)[:4]
+    torch.cuda.synchronize()
+    for name, a, b in zip(("out", "dq", "dk", "dv", "dg"), (out, *grads), want):
+        x, y = a[:, T - tail:].double(), b.double()
+        err = ((x - y).abs().max() / y.abs().max()).item()
+        say(f"    {name}: {err:.2e}")
+        assert err <= (2.0 ** -8 if a.dtype == BF else 1e-5)
+        assert not a[:, :T - tail].any()
 
 
 def test_no_tokens_copies_the_state():

@@ -1318,7 +1318,9 @@ __global__ void __launch_bounds__(64 * JOIN_WAVES) gated_join(float* fst, const 
 //   sum_{t' >= t} q_t' . dq_t' - sum_{s >= t} k_s . dk_s + <S, dL/dS> at the segment's end
 // (a token's product with itself left out of both sums, where it would only cancel).  A
 // workgroup takes one segment of one (b, kv head): at most 16 chunks, four tokens a thread
-// from the last; the sums run in 64 bits, since they cancel.  A gate of 0 passes no gradient.
+// from the last; the sums run in 64 bits, since they cancel.  A gate of 0 passes no gradient,
+// and no pair crosses it: the sums start again there, so that packed sequences leave nothing
+// in each other's gradients, not even what a cancelled sum rounds to.
 struct GateGrad {
     const float* rq;
     const float* rk;
@@ -1332,7 +1334,9 @@ struct GateGrad {
 };
 __global__ void __launch_bounds__(THREADS) gated_gate_grad(GateGrad w) {
     constexpr int N = GATED_MAX_CHUNKS * GC / THREADS;
+    constexpr float ZERO_GATE = -104.f;               // exp of less is zero in fp32
     __shared__ double part[2][4];
+    __shared__ int s_cut[4];
     const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
     int id = xcd_run(blockIdx.x, gridDim.x);
     const int hk = id % w.HK;
@@ -1370,28 +1374,44 @@ __global__ void __launch_bounds__(THREADS) gated_gate_grad(GateGrad w) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) cross += (double)s[j] * (double)r[j];
     }
+    int cut = 0;                                      // a gate of 0 among the tokens so far
 #pragma unroll
     for (int n = 0; n < N; ++n) {
-        sum += v[n];
+        const bool zero = gate[n] < ZERO_GATE;
+        sum = zero ? 0.0 : sum + v[n];
         v[n] = sum;
+        cut |= zero;
     }
-    double s = sum;
+    double s = sum;                                   // sum since the last cut, up to this lane's tokens
+    int f = cut;
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
         const double u = __shfl_up(s, o, 64);
-        if (lane >= o) s += u;
+        const int uf = __shfl_up(f, o, 64);
+        if (lane >= o) {
+            s += f ? 0.0 : u;
+            f |= uf;
+        }
         cross += __shfl_xor(cross, o, 64);
     }
-    if (lane == 63) part[0][wave] = s;
+    if (lane == 63) {
+        part[0][wave] = s;
+        s_cut[wave] = f;
+    }
     if (lane == 0) part[1][wave] = cross;
+    s = __shfl_up(s, 1, 64);
+    f = __shfl_up(f, 1, 64);
     __syncthreads();
-    double before = (part[1][0] + part[1][1]) + (part[1][2] + part[1][3]) + (s - sum);
+    double before = (part[1][0] + part[1][1]) + (part[1][2] + part[1][3]);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) before += k < wave ? part[0][k] : 0.0;
+    for (int k = 0; k < 3; ++k)
+        if (k < wave) before = part[0][k] + (s_cut[k] ? 0.0 : before);
+    if (lane) before = s + (f ? 0.0 : before);
 #pragma unroll
     for (int n = 0; n < N; ++n) {
         const int t = live - 1 - tid * N - n;
-        if (t >= t0) w.dg[(tok0 + t) * w.HK + hk] = gate[n] < -104.f ? 0.f : (float)(before + v[n]);
+        if (gate[n] < ZERO_GATE) before = 0.0;        // v[n] is 0 there, and counts from there on
+        if (t >= t0) w.dg[(tok0 + t) * w.HK + hk] = (float)(before + v[n]);
     }
     for (int t = live + tid; t < t1; t += THREADS) w.dg[(tok0 + t) * w.HK + hk] = 0.f;
 }

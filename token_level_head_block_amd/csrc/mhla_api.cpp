@@ -1084,8 +1084,8 @@ mhla_status gated_backward_impl(const void* q, const void* k, const void* v, con
     const Span in[] = {{q, s.span(s.H, s.qs)}, {k, s.span(s.HK, s.ks)}, {v, s.span(s.HK, s.vs)}, {g, gates},
                        {lens, (size_t)s.B * 4}, {state, s.states()}, {dout, s.rows(s.H)}, {dstate_out, s.states()}};
     const Span outs[] = {{dq, s.rows(s.H)}, {dk, s.rows(s.HK)}, {dv, s.rows(s.HK)}, {dg, gates}, {dstate, s.states()}};
-    const int same[][2] = {{4, 7}};
-    if (spans_clash(in, 8, outs, 5, ws, pl.total, same, 1)) return MHLA_ERR_INVALID_ARG;
+    // dstate may not be dstate_out: that is read to the end of the call
+    if (spans_clash(in, 8, outs, 5, ws, pl.total, nullptr, 0)) return MHLA_ERR_INVALID_ARG;
     bool owned;
     const mhla_status as = take_workspace(&ws, ws_bytes, pl.total, stream, &owned);
     if (as != MHLA_OK) return as;
