@@ -511,10 +511,11 @@ typedef struct mhla_seq {
 } mhla_seq;
 
 /* Validates a sequence problem alone: MHLA_OK, MHLA_ERR_INVALID_ARG (negative
- * counts, H % Hk != 0, a stride below the heads' values, scale not finite),
+ * counts, H no multiple of Hk, one of them 0 alone, a stride below the heads' values, scale not finite),
  * MHLA_ERR_MISALIGNED (a stride that is no multiple of 16 bytes) or
- * MHLA_ERR_UNSUPPORTED (head_dim, dtype, or a size past the limits above or
- * past 2^31 - 1 workgroups). */
+ * MHLA_ERR_UNSUPPORTED (head_dim, dtype, a size past the limits above, or more
+ * than 2796202 blocks of up to 64 value columns over all batch items, kv heads
+ * and segments of a sequence: 1024 tokens each, or fewer where B Hk is small). */
 mhla_status mhla_check_seq(const mhla_seq* seq);
 
 /* Bytes of device workspace (0 for an invalid problem, an empty batch, or a
@@ -591,7 +592,7 @@ typedef struct mhla_rope {
 } mhla_rope;
 
 /* q [B, T, H, d], k [B, T, Hk, d] in seq's dtype and strides (v_stride and
- * scale are not used; kv_heads need not divide heads); positions
+ * scale are not used; kv_heads need not divide heads, and B T < 2^31); positions
  * [B, T, axes] int32; freq [P] fp32; q_out, k_out contiguous.  q_out may be q
  * itself, and k_out k, where these are contiguous.  positions and freq need
  * 4-byte alignment, the other pointers 16.  Needs no workspace. */

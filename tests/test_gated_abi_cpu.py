@@ -31,7 +31,13 @@ def seq(**kw):
     ({"heads": 65538}, UNS), ({"q_stride": 255}, INV), ({"q_stride": 257}, MIS), ({"q_stride": 256}, mh.MHLA_OK),
     ({"k_stride": 120}, INV), ({"v_stride": 132}, MIS), ({"v_stride": (1 << 23) + 8}, UNS), ({"k_stride": -128}, INV),
     ({"batch": 1 << 30, "heads": 2, "kv_heads": 2, "tokens": 1}, UNS),
-    ({"batch": 4, "tokens": 1 << 30, "heads": 64, "kv_heads": 64}, UNS),
+    ({"batch": 4, "tokens": 1 << 30, "heads": 64, "kv_heads": 64}, UNS), ({"heads": 0}, INV),
+    ({"batch": 1398101, "heads": 2, "kv_heads": 2, "tokens": 1}, mh.MHLA_OK),
+    ({"batch": 1398102, "heads": 2, "kv_heads": 2, "tokens": 1}, UNS),
+    ({"batch": 1398101, "heads": 1, "kv_heads": 1, "tokens": 2048}, mh.MHLA_OK),
+    ({"batch": 1398102, "heads": 1, "kv_heads": 1, "tokens": 2048}, UNS),
+    ({"batch": 1, "tokens": 1 << 30, "heads": 2, "kv_heads": 2}, mh.MHLA_OK),
+    ({"batch": (1 << 31) - 1, "tokens": 1 << 30, "heads": 65536, "kv_heads": 65536, "head_dim": 128}, UNS),
 ])
 def test_check_seq(kw, code):
     s = seq(**kw)

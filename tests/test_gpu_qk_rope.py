@@ -191,3 +191,21 @@ def test_chain_of_a_layer():
             err = float(np.linalg.norm(host(a) - b) / np.linalg.norm(b))
             say(f"    {dt} {n}: {err:.2e}")
             assert err <= tol
+
+
+def test_tokens_past_one_launch():
+    """More tokens than the workgroups of one launch take: the last ones are those of a short call."""
+    d, T, tail = 32, (1 << 27) + 5000, 300
+    pos = torch.zeros(1, T, 1, dtype=torch.int32, device="cuda")
+    pos[0, T - tail:, 0] = torch.arange(tail, dtype=torch.int32, device="cuda")
+    freq = 0.5 ** torch.arange(8, device="cuda", dtype=F32)
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    q, k = torch.ones(1, T, 1, d, dtype=BF, device="cuda"), torch.empty(1, T, 0, d, dtype=BF, device="cuda")
+    q[:, T - tail:] = torch.randn(1, tail, 1, d, generator=gen, device="cuda").to(BF)
+    say(f"  [gpu] qk_norm_rope over {T} tokens")
+    qo, _ = mh.qk_norm_rope(q, k, None, None, pos, freq)
+    want, _ = mh.qk_norm_rope(q[:, T - tail:].contiguous(), k[:, T - tail:], None, None, pos[:, T - tail:].contiguous(), freq)
+    torch.cuda.synchronize()
+    assert torch.equal(qo[:, T - tail:], want)
+    # ones of mean square 1, position 0: themselves, to 2^-20
+    assert (qo[:, :T - tail] == 1).all()

@@ -99,7 +99,7 @@ __device__ __forceinline__ Row8 rotate(const Row8& n, const float2* cs, int l, i
 struct Args {
     QkRope r;
     FastDiv div_h, div_hk;
-    int64_t tokens;
+    int64_t first, tokens;  // this launch's first token, and the end of all tokens
     int tile;               // tokens of a workgroup's tile
 };
 
@@ -120,7 +120,7 @@ __global__ void __launch_bounds__(THREADS) qk_rope_fwd(Args a) {
     __shared__ float2 cs[MAX_TOKENS * D / 2];
     const QkRope& r = a.r;
     const int l = threadIdx.x % L, r0 = threadIdx.x / L;
-    const int64_t tok0 = (int64_t)blockIdx.x * a.tile;
+    const int64_t tok0 = a.first + (int64_t)blockIdx.x * a.tile;
     const int n = (int)min((int64_t)a.tile, a.tokens - tok0);
     tile_turns(a, tok0, n, cs);
 #pragma unroll
@@ -249,10 +249,14 @@ __global__ void __launch_bounds__(THREADS) qk_rope_dw(const float* part, int gro
 }
 
 template <typename E, int D>
-hipError_t launch(const Args& a, bool backward) {
+hipError_t launch(Args a, bool backward) {
     if (!backward) {
-        const int64_t n = (a.tokens + a.tile - 1) / a.tile;
-        qk_rope_fwd<E, D><<<dim3((unsigned)n), THREADS, 0, a.r.stream>>>(a);
+        // a launch has fewer than 2^32 threads: more tokens are taken in runs
+        constexpr int64_t MOST = ((int64_t)1 << 32) / THREADS - 1;
+        for (; a.first < a.tokens; a.first += MOST * a.tile) {
+            const int64_t n = (a.tokens - a.first + a.tile - 1) / a.tile;
+            qk_rope_fwd<E, D><<<dim3((unsigned)(n < MOST ? n : MOST)), THREADS, 0, a.r.stream>>>(a);
+        }
         return hipGetLastError();
     }
     qk_rope_bwd<E, D><<<dim3((unsigned)a.r.groups), THREADS, 0, a.r.stream>>>(a);
@@ -268,6 +272,7 @@ int qk_rope_groups(int64_t tokens) { return tokens < 1024 ? (int)tokens : 1024; 
 hipError_t run_qk_rope(const QkRope& r, bool backward) {
     Args a;
     a.r = r;
+    a.first = 0;
     a.tokens = (int64_t)r.B * r.T;
     a.div_h = make_fastdiv((uint32_t)(r.H > 0 ? r.H : 1));
     a.div_hk = make_fastdiv((uint32_t)(r.HK > 0 ? r.HK : 1));

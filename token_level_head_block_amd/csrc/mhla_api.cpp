@@ -897,7 +897,8 @@ mhla_status check_seq(const mhla_seq* q, Seq* s, bool groups) {
     if (q->head_dim != 32 && q->head_dim != 64 && q->head_dim != 128) return MHLA_ERR_UNSUPPORTED;
     if (q->batch < 0 || q->tokens < 0 || q->heads < 0 || q->kv_heads < 0) return MHLA_ERR_INVALID_ARG;
     if (q->tokens > (1 << 30) || q->heads > 65536 || q->kv_heads > 65536) return MHLA_ERR_UNSUPPORTED;
-    if (groups && (q->kv_heads == 0 ? q->heads != 0 : q->heads % q->kv_heads != 0)) return MHLA_ERR_INVALID_ARG;
+    if (groups && (q->kv_heads == 0 || q->heads == 0 ? q->heads != q->kv_heads : q->heads % q->kv_heads != 0))
+        return MHLA_ERR_INVALID_ARG;
     if (!std::isfinite(q->scale)) return MHLA_ERR_INVALID_ARG;
     s->B = q->batch; s->T = q->tokens; s->H = q->heads; s->HK = q->kv_heads; s->D = q->head_dim;
     s->esz = q->dtype == MHLA_F32 ? 4 : 2;
@@ -965,10 +966,12 @@ mhla_status check_gated(const mhla_seq* seq, Seq* s) {
     const mhla_status st = check_seq(seq, s, true);
     if (st != MHLA_OK) return st;
     if (s->empty()) return MHLA_OK;
-    // workgroups of a launch: three walks of a segment's value blocks at most
-    const double walks = (double)s->B * (double)s->HK * mhla::gated_value_blocks((int)s->D);
-    const double segs = (double)s->T / mhla::GATED_CHUNK + 1;
-    if (walks >= 1073741824.0 || walks * segs * 3 >= 2147483648.0) return MHLA_ERR_UNSUPPORTED;
+    // a launch has fewer than 2^32 threads: up to three walks of 512 for each value block and segment
+    constexpr int64_t MOST = ((int64_t)1 << 32) / (3 * 512);
+    const int64_t walks = s->B * s->HK * mhla::gated_value_blocks((int)s->D);
+    if (walks > MOST) return MHLA_ERR_UNSUPPORTED;
+    for (const bool backward : {false, true})
+        if (walks * gated_plan(*s, backward).nseg > MOST) return MHLA_ERR_UNSUPPORTED;
     return MHLA_OK;
 }
 
@@ -1135,7 +1138,7 @@ mhla_status gated_step_impl(const void* q, const void* k, const void* v, const f
 mhla_status check_rope(const mhla_seq* seq, const mhla_rope* rope, Seq* s, int* pairs) {
     const mhla_status st = check_seq(seq, s, false);
     if (st != MHLA_OK) return st;
-    if (s->tokens() >= ((int64_t)1 << 31)) return MHLA_ERR_UNSUPPORTED;   // workgroups of a launch
+    if (s->tokens() >= ((int64_t)1 << 31)) return MHLA_ERR_UNSUPPORTED;
     if (!rope) return MHLA_OK;
     if (rope->style != MHLA_ROPE_HALVES && rope->style != MHLA_ROPE_INTERLEAVED) return MHLA_ERR_INVALID_ARG;
     if (rope->axes < 1 || rope->axes > 3) return MHLA_ERR_INVALID_ARG;
