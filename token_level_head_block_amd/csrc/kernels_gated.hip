@@ -1330,9 +1330,11 @@ struct GateGrad {
     const float* g;
     const int32_t* lens;
     float* dg;
-    int B, T, HK, nx, nb, nseg, seg_chunks, DD;
+    int B, T, HK, nx, nb, nseg, seg_chunks;
 };
+template <int D>
 __global__ void __launch_bounds__(THREADS) gated_gate_grad(GateGrad w) {
+    constexpr int DD = D * D;
     constexpr int N = GATED_MAX_CHUNKS * GC / THREADS;
     constexpr float ZERO_GATE = -104.f;               // exp of less is zero in fp32
     __shared__ double part[2][4];
@@ -1348,31 +1350,56 @@ __global__ void __launch_bounds__(THREADS) gated_gate_grad(GateGrad w) {
     if (w.lens) len = min(max(w.lens[b], 0), T);
     const int t0 = seg * w.seg_chunks * GC, t1 = min(t0 + w.seg_chunks * GC, T), live = max(min(t1, len), t0);
     const int64_t tok0 = (int64_t)b * T, tokens = (int64_t)w.B * T;
-    // this thread's tokens, descending: thread 0 has the last ones
+    // this thread's tokens, descending: thread 0 has the last ones.  Loads of all four are under
+    // way at once, those behind the segment's start with an address in it
+    const int last = live - 1 - tid * N;
     double v[N];
     float gate[N];
     double sum = 0.0;
 #pragma unroll
     for (int n = 0; n < N; ++n) {
-        const int t = live - 1 - tid * N - n;
         v[n] = 0.0;
         gate[n] = 0.f;
-        if (t >= t0) {
-            const int64_t tk = tok0 + t;
-            gate[n] = w.g[tk * w.HK + hk];
-            for (int e = 0; e < w.nb; ++e) {
-                for (int h = 0; h < w.nx; ++h) v[n] += (double)w.rq[((e * tokens + tk) * w.HK + hk) * w.nx + h];
-                v[n] -= (double)w.rk[(e * tokens + tk) * w.HK + hk];
-            }
-        }
     }
-    const float* S = w.fst + pair * w.fst_pair + (int64_t)seg * w.DD;
-    const float* R = w.rst + (pair * w.nseg + seg) * w.DD;
-    double cross = 0.0;
-    for (int i = tid * 4; w.rst && i < w.DD; i += THREADS * 4) {
-        const f32x4 s = load4(S + i), r = load4(R + i);
+    if (live > t0) {
+        int64_t tk[N];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) cross += (double)s[j] * (double)r[j];
+        for (int n = 0; n < N; ++n) {
+            tk[n] = (tok0 + max(last - n, t0)) * w.HK + hk;
+            gate[n] = w.g[tk[n]];
+        }
+        const int64_t block = tokens * w.HK;
+        for (int e = 0; e < w.nb; ++e) {
+            for (int h = 0; h < w.nx; ++h)
+#pragma unroll
+                for (int n = 0; n < N; ++n) v[n] += (double)w.rq[(e * block + tk[n]) * w.nx + h];
+#pragma unroll
+            for (int n = 0; n < N; ++n) v[n] -= (double)w.rk[e * block + tk[n]];
+        }
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+            if (last - n < t0) {
+                v[n] = 0.0;
+                gate[n] = 0.f;
+            }
+    }
+    double cross = 0.0;
+    if (w.rst) {
+        const float* S = w.fst + pair * w.fst_pair + (int64_t)seg * DD;
+        const float* R = w.rst + (pair * w.nseg + seg) * DD;
+        constexpr int RUN = THREADS * 4, UN = DD / RUN < 4 ? DD / RUN : 4;
+        for (int i = tid * 4; i < DD; i += UN * RUN) {
+            f32x4 x[UN], y[UN];
+#pragma unroll
+            for (int u = 0; u < UN; ++u) {
+                x[u] = load4(S + i + u * RUN);
+                y[u] = load4(R + i + u * RUN);
+            }
+#pragma unroll
+            for (int u = 0; u < UN; ++u)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) cross += (double)x[u][j] * (double)y[u][j];
+        }
     }
     int cut = 0;                                      // a gate of 0 among the tokens so far
 #pragma unroll
@@ -1409,7 +1436,7 @@ __global__ void __launch_bounds__(THREADS) gated_gate_grad(GateGrad w) {
     if (lane) before = s + (f ? 0.0 : before);
 #pragma unroll
     for (int n = 0; n < N; ++n) {
-        const int t = live - 1 - tid * N - n;
+        const int t = last - n;
         if (gate[n] < ZERO_GATE) before = 0.0;        // v[n] is 0 there, and counts from there on
         if (t >= t0) w.dg[(tok0 + t) * w.HK + hk] = (float)(before + v[n]);
     }
@@ -1685,8 +1712,8 @@ hipError_t backward(const GatedBackward& f) {
     d.rst = p.nseg > 1 ? f.rst : f.ds1;
     d.lens = p.lens; d.dg = f.dg;
     d.B = p.B; d.T = p.T; d.HK = p.HK; d.nx = G; d.nb = gated_value_blocks(D); d.nseg = p.nseg;
-    d.seg_chunks = p.seg_chunks; d.DD = DD;
-    gated_gate_grad<<<dim3((unsigned)((int64_t)p.B * p.HK * p.nseg)), THREADS, 0, p.stream>>>(d);
+    d.seg_chunks = p.seg_chunks;
+    gated_gate_grad<D><<<dim3((unsigned)((int64_t)p.B * p.HK * p.nseg)), THREADS, 0, p.stream>>>(d);
     return hipGetLastError();
 }
 
