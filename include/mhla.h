@@ -478,8 +478,8 @@ mhla_status mhla_layer_forward(const void* x, const float* W, const mhla_grid* g
  *
  * Tensors (device pointers):
  *   q, dq, out, dout  [B, T, H, d]     k, v, dk, dv  [B, T, Hk, d]
- *   g, dg             [B, T, Hk] fp32  (log gates: -infinity forgets the state,
- *                                       so it starts a sequence of its own)
+ *   g, dg             [B, T, Hk] fp32  (log gates, at most 0: -infinity forgets the
+ *                                       state, so it starts a sequence of its own)
  *   states            [B, Hk, d, d] fp32, element [c][e] from key value c and
  *                     value value e
  *   lens              [B] int32 or NULL: sequence b has min(max(lens[b], 0), T)
@@ -492,6 +492,9 @@ mhla_status mhla_layer_forward(const void* x, const float* W, const mhla_grid* g
  * its own chunk (64 tokens, counted from the sequence's start), earlier tokens
  * among them, and of all later tokens, past a gate of 0 too; never those of
  * another sequence.
+ *
+ * Gates above 0 are not refused: they are computed as given while the gates'
+ * products over any run of tokens inside a chunk stay in fp32's range.
  *
  * Precision: states, gate sums and dg are fp32 sums of products as precise as
  * in fp32; bf16 tensors are rounded once, at the end.  No atomics: results

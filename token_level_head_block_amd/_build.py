@@ -30,7 +30,7 @@ COMMON = ["-x", "hip", f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC",
 
 
 # Matrix-core results in ordinary registers where the kernel keeps working on them: moves
-# between the two register files were an eighth of the walk's vector instructions.
+# between the two register files were 104 of about 670 vector instructions of a walk's chunk.
 SOURCE_FLAGS = {"kernels_gated.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]}
 
 

@@ -63,17 +63,6 @@ hipError_t run_gated_backward(const GatedBackward& f);
 constexpr int gated_value_block(int D) { return D < 64 ? D : 64; }
 inline int gated_value_blocks(int D) { return D / gated_value_block(D); }
 
-// Walks (workgroups) of a split sequence for each compute unit, about as many as it holds by
-// registers and LDS.  Measured with 1, 2 and 3: forwards one sequence of 65536 tokens, 6 heads
-// of 64 bf16: 96, 80, 82 us; 2 x 4096 tokens, 70 heads of 32 fp32: 171, 138, 122 us; backwards
-// 2 x 4097 tokens, 12 heads over 4 of 128: 182, 168, 176 us; 4 x 4096, 8 heads of 64 fp32:
-// 219, 228, 257 us.
-inline int gated_walks_per_cu(bool bf16, int D, bool backward) {
-    if (D == 128) return bf16 ? 2 : 1;
-    if (backward) return bf16 || D == 32 ? 2 : 1;
-    return D == 32 ? 3 : 2;
-}
-
 struct GatedStep {
     int B, H, HK, D;
     bool bf16;

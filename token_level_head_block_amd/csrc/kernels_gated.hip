@@ -484,8 +484,14 @@ __device__ __forceinline__ int xcd_run(int blk, int n) {
 // other has the state in its accumulators, adds the chunk to it, and brings the next tiles.
 // Between two barriers, while the outputs are stored, it replaces tiles and state.  As eight
 // waves the two shorter chains of a chunk run at once and fit 128 registers, four waves a
-// SIMD; one group doing both took 1.6 times as long (forwards at head_dim 64, and more
-// backwards).
+// SIMD (whole calls, one group doing both and two: forwards 65536 tokens, 6 heads of 64 bf16
+// 82.4 and 79 us; 2 x 4096 tokens, 70 heads of 32 fp32 129 and 122; backwards 65536 tokens 232
+// and 221).
+// What bounds it: at D <= 64 in bf16 the tokens' bytes (65536 tokens, 6 heads of 64: 47 us
+// forwards, 201 MB at 4.3 TB/s, the matrix cores busy a fifth of it); in fp32 the matrix cores,
+// whose 16x16x4 products of a chunk take half of the time (70 heads of 32: 89 us, 294 MB at 3.3
+// TB/s); where a walk is one of few, its chain of barriers, loads and products, 1.6 us a chunk
+// at D = 128 (4 x 1000 tokens, 2 kv heads of 128: 13 us).
 // Products are formed transposed (Y X^T, then Z^T P^T), so that P leaves the accumulators as
 // the next product's operand and a lane stores four neighbouring values of one token.
 // P and S are taken as two bf16 terms (three for the sums r, which are fp32 results), so
@@ -823,10 +829,15 @@ __global__ void __launch_bounds__((walk_threads<E, D>()), (!split_walk<E, D>() |
 // Backwards over a segment with X = k and v, Y = q, Z = do: the pair products q . k and
 // do . v serve dk, dv and k . dk alike, the tiles are read once and the state's gradient D is
 // summed once, where two walks would do each twice.  D lies in LDS once, transposed ([e][c]):
-// dv contracts it over c (its columns), dk over e (its rows, by transposing reads).  D <= 64: at 128 the state of all columns leaves room for one
-// workgroup of a compute unit, and dk and dv are walks of their own.
+// dv contracts it over c (its columns), dk over e (its rows, by transposing reads).  D <= 64:
+// at 128 the state of all columns leaves room for one workgroup of a compute unit, and dk and
+// dv are walks of their own.
 // One group of waves computes dk and k . dk and brings the tiles of q, the other dv, with D
 // in its accumulators, and the tiles of do.
+// Bound by vector instructions and LDS reads together: at 65536 tokens, 6 heads of 64 bf16 the
+// launch of all gradients takes 171 us, 538 MB at 3.1 TB/s, with the vector units busy half of
+// it, LDS two fifths (a third of that are bank conflicts of the transposing reads of
+// interleaved tiles) and the matrix cores a fifth.
 struct Back {
     Role q, k, v, dout;
     void* dk;
@@ -1132,7 +1143,9 @@ __device__ __forceinline__ void back(const Back& w, int id, char* lds) {
 
 // All three gradients in one launch: the walks for dq and for dk and dv (at D = 128 for dv
 // and for dk) do not wait for each other, short problems run them side by side and long ones
-// fill the last round.  The walks of one segment have neighbouring numbers, the longest first.
+// fill the last round (2 x 4097 tokens, 12 heads over 4 of 128, whole call: 196 us in launches
+// of their own, 165 in one).  The walks of one segment have neighbouring numbers, the longest
+// first; numbered from the last they took as long.
 struct Grads {
     Walk q, v, k;   // D = 128: v and k
     Back kv;        // D <= 64
@@ -1160,7 +1173,9 @@ __global__ void __launch_bounds__((walk_threads<E, D>()), (!split_walk<E, D>() ?
 // ---------------------------------------------------------------- segments
 // What each segment adds to the state, from zero, for the forward state (Y = k, Z = v) and,
 // with two roles, for the backward one (Y = q, Z = do of all the group's heads), and the
-// segment's decay.
+// segment's decay.  Bound by the bytes of what it reads: 65536 tokens, 6 heads of 64 bf16: 26 us
+// for 101 MB (3.9 TB/s) with one role, 40 us for 201 MB (5.0) with two; a wave has its state
+// tiles in registers and stages the next chunk's rows while it adds this one's.
 struct Local {
     Role y[2], z[2];
     int ny[2];
@@ -1255,7 +1270,10 @@ __global__ void __launch_bounds__(THREADS) gated_local(Local w) {
 // Joins the segments: fst[j] becomes the state before segment j (j = nseg: after the last),
 // rst[j] the gradient of the state after segment j.  A workgroup has 64 elements of one
 // pair's states, each of its waves a run of up to JOIN_RUN segments of them: all of a run's
-// loads are in flight at once, the runs are joined through LDS.
+// loads are in flight at once, the runs are joined through LDS.  Bound by its states' bytes and,
+// where they are few, by the latency of one read, one exchange and one write: 79 segments of 6
+// heads of 64 forwards 6.4 us (16 MB), both ways 9.7 us (31 MB); 8 pairs of 128, 22 segments both
+// ways 11.3 us (46 MB at 4.1 TB/s).
 constexpr int JOIN_WAVES = 16, JOIN_RUN = 16;
 __global__ void __launch_bounds__(64 * JOIN_WAVES) gated_join(float* fst, const float* s0, float* rst, const float* ds1,
                                                              const float* dec, int nseg, int DD) {
@@ -1321,6 +1339,8 @@ __global__ void __launch_bounds__(64 * JOIN_WAVES) gated_join(float* fst, const 
 // from the last; the sums run in 64 bits, since they cancel.  A gate of 0 passes no gradient,
 // and no pair crosses it: the sums start again there, so that packed sequences leave nothing
 // in each other's gradients, not even what a cancelled sum rounds to.
+// Bound by latency: few bytes, and two rounds of loads (65536 tokens, 6 heads of 64: 9.4 us; 2 x
+// 4097, 12 heads over 4 of 128: 8.4 us, 15.8 with the loads one after the other).
 struct GateGrad {
     const float* rq;
     const float* rk;
@@ -1446,7 +1466,10 @@ __global__ void __launch_bounds__(THREADS) gated_gate_grad(GateGrad w) {
 // ---------------------------------------------------------------- one token
 // S' = exp(g) S + k v^T in place, o = scale S'^T q.  Bound by the state's bytes: read and
 // written once.  A workgroup has EB value columns of one (row, kv head): a thread four
-// columns of every RG-th key row, sixteen bytes a load, the whole state's share in registers.
+// columns of every RG-th key row, sixteen bytes a load, the whole state's share in registers,
+// so that every byte is asked for before the first is needed.  240 rows of 12 heads of 128,
+// 377 MB: 80 us, 4.7 TB/s (the same pool over and over, from the last-level cache: 56 us); one row
+// of 6 heads of 64: 3.3 us.
 // Rows that name the same slot are that sequence's next tokens, in the order of the rows:
 // the first of them does them all, the others leave.
 template <typename E, int D, int EB>

@@ -7,6 +7,7 @@
 // in kernels_bf16.hip and kernels_f32.hip.
 #include <mhla.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <cstdlib>
@@ -917,31 +918,61 @@ mhla_status check_seq(const mhla_seq* q, Seq* s, bool groups) {
 }
 
 // Segments of a sequence: workgroups walk them side by side, for one more pass over the keys
-// and values and a state a segment written and read.  Forwards a sequence is split where
-// there is less than a walk for each of 256 compute units (16 x 4096 tokens, 16 heads of 64:
-// one segment 144 us, two 212), into about as many walks as run at once (a few more would run
-// as a second round, as long as the first), and not at all up to FEW chunks, which one walk
-// goes through in the time of the two launches that splitting adds (4 heads, one segment and
-// split: 512 tokens of 64 bf16 forwards 16.3 and 19.1 us; 256 tokens of 128 bf16 forwards 15.5
-// and 19.0, backwards 30.4 and 32.5; 128 tokens of 128 fp32 forwards 19.1 and 20.4).  The plan
-// fixes the workspace, so it goes by the problem alone.
+// and values and a state a segment written and read.  The number of segments is the one of
+// least time by this count, in times of a chunk: a workgroup takes its chunks and BEGIN to
+// start and end; a compute unit that has two at a time takes `pair` times as long as with one,
+// and `odd` for a third; all wait for the one with the most; splitting costs a pass over all
+// tokens, at one chunk a compute unit (less at D = 32), and a launch.  The factors are fitted to
+// about 200 problems of 2 to 640 walks and 6 to 1024 chunks, in all types, sizes and both
+// directions: the choice takes 1.5% more than the best of about 15 numbers of segments (at
+// worst 17%); as many segments as two walks a compute unit, or one from 256 walks on, took
+// 7% more (at worst 67%: 350 tokens, 75 heads of 128 bf16 forwards).  A sequence of up to `few` chunks is not
+// split: one walk goes through it in the time of the two launches that splitting adds (4
+// heads, one segment and split: 512 tokens of 64 bf16 forwards 16.3 and 19.1 us; 256 tokens of
+// 128 bf16 forwards 15.5 and 19.0, backwards 30.4 and 32.5; 128 tokens of 128 fp32 forwards
+// 19.1 and 20.4).
+// Backwards with several query heads to a kv head and D other than 64, where the three kinds
+// of walks differ most, an even spread counts for more than whole rounds: about two walks of
+// each kind a compute unit (one in fp32 at D = 128; 2 x 4097 tokens, 12 heads over 4 of 128 in 22
+// and 10 segments: 150 and 165 us; 12000 tokens, 8 over 1 in 188 and 63: 121 and 148).
 // Backwards, segments of at most MOST chunks: the gates' gradients start anew from <S, dS>
-// at each segment's end.
+// at each segment's end.  The plan fixes the workspace, so it goes by the problem alone.
 struct GatedPlan {
     int nseg, seg_chunks;
     size_t fst, rst, dec, rq, rk, total;
 };
 GatedPlan gated_plan(const Seq& s, bool backward) {
-    constexpr int64_t CUS = 256, MOST = mhla::GATED_MAX_CHUNKS;
+    constexpr int64_t CUS = 256, MOST = mhla::GATED_MAX_CHUNKS, ROUNDS = 8;
+    constexpr double BEGIN = 0.75;
     const int64_t C = mhla::GATED_CHUNK, chunks = s.T > 0 ? (s.T + C - 1) / C : 1;
     const int64_t walks = s.B * s.HK * mhla::gated_value_blocks((int)s.D);
     const bool bf16 = s.esz == 2;
     const int64_t few = !bf16 && s.D == 128 ? 2 : bf16 && s.D <= 64 && !backward ? 8 : 4;
-    int64_t n = CUS * mhla::gated_walks_per_cu(bf16, (int)s.D, backward) / walks;
-    if ((!backward && walks >= CUS) || chunks <= few) n = 1;
-    if (n > chunks) n = chunks;
-    if (backward && n < (chunks + MOST - 1) / MOST) n = (chunks + MOST - 1) / MOST;
-    if (n < 1) n = 1;
+    const int64_t least = backward ? (chunks + MOST - 1) / MOST : 1;
+    int64_t n = 1;
+    if (chunks > few && backward && s.H > s.HK && s.D != 64) {
+        n = CUS * (!bf16 && s.D == 128 ? 1 : 2) / walks;
+    } else if (chunks > few) {
+        // workgroups of a segment, in walks
+        const int64_t kinds = !backward ? walks : s.D <= 64 ? 2 * walks : 3 * walks;
+        const double pair = s.D == 32 ? 1.8 : bf16 ? 1.5 : 1.65, odd = s.D == 32 ? 0.85 : 1.0;
+        const double split = (s.D == 32 ? 0.4 : 1.0) * (double)(chunks * walks) / CUS + BEGIN;
+        double best = 0.0;
+        for (int64_t r = 0; r <= ROUNDS; ++r) {
+            // as many segments as fit r workgroups a compute unit
+            int64_t m = std::min(std::max(CUS * r / kinds, least), chunks);
+            const int64_t each = (chunks + m - 1) / m;
+            m = (chunks + each - 1) / each;
+            const int64_t full = (m * kinds + CUS - 1) / CUS;
+            const double wait = full > 1 ? pair * (double)(full / 2) + odd * (double)(full & 1) : 1.0;
+            const double t = wait * ((double)each + BEGIN) + (m > 1 ? split : 0.0);
+            if (r == 0 || t < best) {
+                best = t;
+                n = m;
+            }
+        }
+    }
+    n = std::max<int64_t>(std::min(std::max(n, least), chunks), 1);
     GatedPlan p;
     p.seg_chunks = (int)((chunks + n - 1) / n);
     p.nseg = (int)((chunks + p.seg_chunks - 1) / p.seg_chunks);
@@ -970,6 +1001,7 @@ mhla_status check_gated(const mhla_seq* seq, Seq* s) {
     constexpr int64_t MOST = ((int64_t)1 << 32) / (3 * 512);
     const int64_t walks = s->B * s->HK * mhla::gated_value_blocks((int)s->D);
     if (walks > MOST) return MHLA_ERR_UNSUPPORTED;
+    if (walks * (s->T / mhla::GATED_CHUNK + 1) <= MOST) return MHLA_OK;
     for (const bool backward : {false, true})
         if (walks * gated_plan(*s, backward).nseg > MOST) return MHLA_ERR_UNSUPPORTED;
     return MHLA_OK;
