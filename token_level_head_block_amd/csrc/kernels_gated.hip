@@ -486,12 +486,12 @@ __device__ __forceinline__ int xcd_run(int blk, int n) {
 // waves the two shorter chains of a chunk run at once and fit 128 registers, four waves a
 // SIMD (whole calls, one group doing both and two: forwards 65536 tokens, 6 heads of 64 bf16
 // 82.4 and 79 us; 2 x 4096 tokens, 70 heads of 32 fp32 129 and 122; backwards 65536 tokens 232
-// and 221).
+// and 221, both with 79 segments).
 // What bounds it: at D <= 64 in bf16 the tokens' bytes (65536 tokens, 6 heads of 64: 47 us
 // forwards, 201 MB at 4.3 TB/s, the matrix cores busy a fifth of it); in fp32 the matrix cores,
 // whose 16x16x4 products of a chunk take half of the time (70 heads of 32: 89 us, 294 MB at 3.3
-// TB/s); where a walk is one of few, its chain of barriers, loads and products, 1.6 us a chunk
-// at D = 128 (4 x 1000 tokens, 2 kv heads of 128: 13 us).
+// TB/s); where walks are few and short, the chain from the first load through state, products
+// and stores (4 x 1000 tokens, 8 heads over 2 of 128, one chunk each: 13 us).
 // Products are formed transposed (Y X^T, then Z^T P^T), so that P leaves the accumulators as
 // the next product's operand and a lane stores four neighbouring values of one token.
 // P and S are taken as two bf16 terms (three for the sums r, which are fp32 results), so
@@ -835,7 +835,7 @@ __global__ void __launch_bounds__((walk_threads<E, D>()), (!split_walk<E, D>() |
 // One group of waves computes dk and k . dk and brings the tiles of q, the other dv, with D
 // in its accumulators, and the tiles of do.
 // Bound by vector instructions and LDS reads together: at 65536 tokens, 6 heads of 64 bf16 the
-// launch of all gradients takes 171 us, 538 MB at 3.1 TB/s, with the vector units busy half of
+// launch of all gradients takes 157 us, 538 MB at 3.4 TB/s, with the vector units busy half of
 // it, LDS two fifths (a third of that are bank conflicts of the transposing reads of
 // interleaved tiles) and the matrix cores a fifth.
 struct Back {
@@ -1174,7 +1174,7 @@ __global__ void __launch_bounds__((walk_threads<E, D>()), (!split_walk<E, D>() ?
 // What each segment adds to the state, from zero, for the forward state (Y = k, Z = v) and,
 // with two roles, for the backward one (Y = q, Z = do of all the group's heads), and the
 // segment's decay.  Bound by the bytes of what it reads: 65536 tokens, 6 heads of 64 bf16: 26 us
-// for 101 MB (3.9 TB/s) with one role, 40 us for 201 MB (5.0) with two; a wave has its state
+// for 101 MB (3.9 TB/s) with one role, 43 us for 201 MB (4.7) with two; a wave has its state
 // tiles in registers and stages the next chunk's rows while it adds this one's.
 struct Local {
     Role y[2], z[2];
@@ -1272,7 +1272,7 @@ __global__ void __launch_bounds__(THREADS) gated_local(Local w) {
 // pair's states, each of its waves a run of up to JOIN_RUN segments of them: all of a run's
 // loads are in flight at once, the runs are joined through LDS.  Bound by its states' bytes and,
 // where they are few, by the latency of one read, one exchange and one write: 79 segments of 6
-// heads of 64 forwards 6.4 us (16 MB), both ways 9.7 us (31 MB); 8 pairs of 128, 22 segments both
+// heads of 64 forwards 6.3 us (16 MB), 128 both ways 12.5 us (50 MB at 4.0 TB/s); 8 pairs of 128, 22 segments both
 // ways 11.3 us (46 MB at 4.1 TB/s).
 constexpr int JOIN_WAVES = 16, JOIN_RUN = 16;
 __global__ void __launch_bounds__(64 * JOIN_WAVES) gated_join(float* fst, const float* s0, float* rst, const float* ds1,
@@ -1339,7 +1339,7 @@ __global__ void __launch_bounds__(64 * JOIN_WAVES) gated_join(float* fst, const 
 // from the last; the sums run in 64 bits, since they cancel.  A gate of 0 passes no gradient,
 // and no pair crosses it: the sums start again there, so that packed sequences leave nothing
 // in each other's gradients, not even what a cancelled sum rounds to.
-// Bound by latency: few bytes, and two rounds of loads (65536 tokens, 6 heads of 64: 9.4 us; 2 x
+// Bound by latency: few bytes, and two rounds of loads (65536 tokens, 6 heads of 64: 10.1 us; 2 x
 // 4097, 12 heads over 4 of 128: 8.4 us, 15.8 with the loads one after the other).
 struct GateGrad {
     const float* rq;

@@ -926,11 +926,11 @@ mhla_status check_seq(const mhla_seq* q, Seq* s, bool groups) {
 // about 200 problems of 2 to 640 walks and 6 to 1024 chunks, in all types, sizes and both
 // directions: the choice takes 1.5% more than the best of about 15 numbers of segments (at
 // worst 17%); as many segments as two walks a compute unit, or one from 256 walks on, took
-// 7% more (at worst 67%: 350 tokens, 75 heads of 128 bf16 forwards).  A sequence of up to `few` chunks is not
-// split: one walk goes through it in the time of the two launches that splitting adds (4
-// heads, one segment and split: 512 tokens of 64 bf16 forwards 16.3 and 19.1 us; 256 tokens of
-// 128 bf16 forwards 15.5 and 19.0, backwards 30.4 and 32.5; 128 tokens of 128 fp32 forwards
-// 19.1 and 20.4).
+// 7% more (at worst 67%: 350 tokens, 75 heads of 128 bf16 forwards).  A sequence of up to
+// `few` chunks is not split: one walk goes through it in the time of the two launches that
+// splitting adds (4 heads, one segment and split: 512 tokens of 64 bf16 forwards 16.3 and 19.1
+// us; 256 tokens of 128 bf16 forwards 15.5 and 19.0, backwards 30.4 and 32.5; 128 tokens of 128
+// fp32 forwards 19.1 and 20.4).
 // Backwards with several query heads to a kv head and D other than 64, where the three kinds
 // of walks differ most, an even spread counts for more than whole rounds: about two walks of
 // each kind a compute unit (one in fp32 at D = 128; 2 x 4097 tokens, 12 heads over 4 of 128 in 22
