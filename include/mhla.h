@@ -523,9 +523,9 @@ mhla_status mhla_check_seq(const mhla_seq* seq);
 
 /* Bytes of device workspace (0 for an invalid problem, an empty batch, or a
  * problem that needs none).  From the start, at 256-byte boundaries, for the
- * segments a sequence is split into: states before each segment and after the
- * last, segment decays, and backwards the states' gradients behind each
- * segment and the per-token sums that dg is made of. */
+ * segments a sequence is split into: states before each segment (backwards
+ * also after the last), segment decays, and backwards the states' gradients
+ * behind each segment and the per-token sums that dg is made of. */
 size_t mhla_gated_workspace_bytes(const mhla_seq* seq);
 size_t mhla_gated_backward_workspace_bytes(const mhla_seq* seq);
 

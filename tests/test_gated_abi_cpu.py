@@ -110,7 +110,7 @@ def test_workspace_holds_segment_states():
     assert mh.mhla_gated_workspace_bytes(short) == 0
     assert mh.mhla_gated_backward_workspace_bytes(short) == up(64 * 64 * 4) + 2 * up(256 * 4)
     few = mh.make_seq(1, 64 * 9, 1, 1, 64, mh.MHLA_BF16)         # a segment a chunk
-    assert mh.mhla_gated_workspace_bytes(few) == up(10 * 64 * 64 * 4) + up(9 * 4)
+    assert mh.mhla_gated_workspace_bytes(few) == up(9 * 64 * 64 * 4) + up(9 * 4)
     n = up(10 * 64 * 64 * 4) + up(9 * 4) + up(9 * 64 * 64 * 4) + 2 * up(576 * 4)
     assert mh.mhla_gated_backward_workspace_bytes(few) == n
 

@@ -29,16 +29,16 @@ struct GatedProblem {
     hipStream_t stream;
 };
 
-// Workspace regions of a split sequence (nseg > 1): for every (b, kv head) nseg + 1
-// (before each segment, and after the last) or nseg (after each segment) states of D x D
-// fp32 and nseg segment decays.  Backwards with one segment fst holds the state after the
-// sequence alone (where the final state's gradient is given).
+// Workspace regions of a split sequence (nseg > 1): for every (b, kv head) states of D x D
+// fp32, before each segment (backwards also after the last) and, backwards, their gradients
+// after each segment, and the segments' decays.  Backwards with one segment fst holds the
+// state after the sequence alone (where the final state's gradient is given).
 struct GatedForward {
     GatedProblem p;
     void* out;
     float* s1;     // [B, HK, D, D] or nullptr
-    float* fst;    // [B*HK][nseg + 1][D*D] (nseg > 1)
-    float* fdec;   // [B*HK][nseg]
+    float* fst;    // [B*HK][nseg][D*D] (nseg > 1)
+    float* fdec;   // [B*HK][nseg - 1], of nseg
 };
 hipError_t run_gated_forward(const GatedForward& f);
 

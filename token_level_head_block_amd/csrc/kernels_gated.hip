@@ -1592,21 +1592,23 @@ hipError_t forward(const GatedForward& f) {
     const GatedProblem& p = f.p;
     hipError_t err = hipSuccess;
     if (p.nseg > 1) {
+        // the walks need the state before each segment: nobody that of the last one alone
+        const int before = p.nseg - 1;
         Local l = {};
         l.roles = 1;
         l.y[0] = {p.k, p.ks};
         l.z[0] = {p.v, p.vs};
         l.ny[0] = 1;
         l.st[0] = f.fst;
-        l.pair[0] = (int64_t)(p.nseg + 1) * D * D;
+        l.pair[0] = (int64_t)p.nseg * D * D;
         l.first[0] = D * D;
         l.key_scale[0] = 1.f;
         l.dec = f.fdec;
         l.g = p.g;
         l.lens = p.lens;
-        l.B = p.B; l.T = p.T; l.HK = p.HK; l.nseg = p.nseg; l.seg_chunks = p.seg_chunks;
+        l.B = p.B; l.T = p.T; l.HK = p.HK; l.nseg = before; l.seg_chunks = p.seg_chunks;
         if ((err = launch_local<E, D>(l, p.stream)) != hipSuccess) return err;
-        if ((err = launch_join(f.fst, p.s0, nullptr, nullptr, f.fdec, p.B * p.HK, p.nseg, D * D, p.stream)) != hipSuccess)
+        if ((err = launch_join(f.fst, p.s0, nullptr, nullptr, f.fdec, p.B * p.HK, before, D * D, p.stream)) != hipSuccess)
             return err;
     }
     Walk w = {};
@@ -1617,7 +1619,7 @@ hipError_t forward(const GatedForward& f) {
     w.g = p.g;
     w.lens = p.lens;
     w.start = p.nseg > 1 ? f.fst : p.s0;
-    w.start_pair = p.nseg > 1 ? (int64_t)(p.nseg + 1) * D * D : D * D;
+    w.start_pair = (int64_t)p.nseg * D * D;
     w.start_seg = D * D;
     w.end = f.s1;
     w.sc = D; w.se = 1;

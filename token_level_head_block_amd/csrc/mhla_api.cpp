@@ -980,7 +980,7 @@ GatedPlan gated_plan(const Seq& s, bool backward) {
     const size_t nb = (size_t)mhla::gated_value_blocks((int)s.D);
     const size_t split = p.nseg > 1 ? 1 : 0;
     p.fst = 0;
-    p.dec = p.fst + align_up(pairs * (split ? (size_t)(p.nseg + 1) : (size_t)backward) * state);
+    p.dec = p.fst + align_up(pairs * (split ? (size_t)(p.nseg + (backward ? 1 : 0)) : (size_t)backward) * state);
     p.rst = p.dec + split * align_up(pairs * (size_t)p.nseg * 4);
     if (!backward) {
         p.rq = p.rk = p.rst;
