@@ -909,7 +909,7 @@ mhla_status check_seq(const mhla_seq* q, Seq* s, bool groups) {
     for (int i = 0; i < 3; ++i) {
         *out[i] = in[i] == 0 ? least[i] : in[i];
         if (*out[i] < least[i]) return MHLA_ERR_INVALID_ARG;
-        if (*out[i] * (int64_t)s->esz % 16 != 0) return MHLA_ERR_MISALIGNED;
+        if (*out[i] % (16 / (int64_t)s->esz) != 0) return MHLA_ERR_MISALIGNED;
         if (*out[i] > (1 << 23)) return MHLA_ERR_UNSUPPORTED;   // the kernels' 32-bit offsets in a chunk of 64 tokens
         // every tensor's bytes stay within 2^62
         if ((double)s->B * (double)s->T * (double)*out[i] * 4.0 > 4.6e18) return MHLA_ERR_UNSUPPORTED;
