@@ -7,7 +7,12 @@ import subprocess
 
 import pytest
 
-from test_abi_sanitized import CLANG, CSRC, HIPCC, OBJ, ROOT, SAN
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+CSRC = os.path.join(ROOT, "token_level_head_block_amd", "csrc")
+OBJ = os.path.join(ROOT, "_build")
+HIPCC = "/opt/rocm/bin/hipcc"
+CLANG = "/opt/rocm/llvm/bin/clang++"
+SAN = ["-fsanitize=address,undefined", "-fno-sanitize-recover=all", "-fno-omit-frame-pointer"]
 
 
 @pytest.mark.skipif(not (os.path.exists(HIPCC) and os.path.exists(CLANG)), reason="ROCm toolchain not present")
