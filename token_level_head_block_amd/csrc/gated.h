@@ -38,7 +38,7 @@ struct GatedForward {
     void* out;
     float* s1;     // [B, HK, D, D] or nullptr
     float* fst;    // [B*HK][nseg][D*D] (nseg > 1)
-    float* fdec;   // [B*HK][nseg - 1], of nseg
+    float* fdec;   // [B*HK][nseg - 1]
 };
 hipError_t run_gated_forward(const GatedForward& f);
 
